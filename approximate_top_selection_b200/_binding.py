@@ -18,6 +18,19 @@ from . import build as _build
 TOPK_OK, TOPK_EINVAL, TOPK_EUNSUPPORTED, TOPK_ECUDA, TOPK_EWORKSPACE, TOPK_ESCRATCH = range(6)
 TOPK_OP_BUCKETED, TOPK_OP_EXACT, TOPK_OP_SCORE, TOPK_OP_BUCKETED_BF16 = range(4)
 
+TOPK_CACHE_BF16, TOPK_CACHE_E4M3 = range(2)
+
+
+class TopkCache(ctypes.Structure):
+    """topk_cache of include/topk_b200.h."""
+
+    _fields_ = [("data", ctypes.c_void_p), ("scale", ctypes.c_void_p), ("pages", ctypes.c_int64),
+                ("kv_heads", ctypes.c_int), ("page_size", ctypes.c_int), ("d", ctypes.c_int),
+                ("type", ctypes.c_int)] + [(n, ctypes.c_int64) for n in (
+                    "page_stride", "head_stride", "token_stride", "scale_page_stride", "scale_head_stride",
+                    "scale_token_stride")]
+
+
 _lib = None
 _lock = threading.Lock()
 
@@ -72,6 +85,22 @@ def load_library():
             lib.topk_sample.restype = i32
             lib.topk_sample_bf16.argtypes = [p, i64, i64, i32, i32, i32, f32, p, p, p, p, p, sz, p]
             lib.topk_sample_bf16.restype = i32
+            c = ctypes.POINTER(TopkCache)
+            lib.cache_write.argtypes = [p, i64, i64, p, i64, i64, i64, c, c, p, p]
+            lib.cache_write.restype = i32
+            lib.cache_read.argtypes = [c, p, i64, i32, p, i64, i64, p, p]
+            lib.cache_read.restype = i32
+            lib.paged_attention.argtypes = [p, i64, i64, i32, c, c, p, i64, i32, p, p, i32, i32, f32, p, p, p, sz, p]
+            lib.paged_attention.restype = i32
+            lib.paged_attention_workspace_bytes.argtypes = [i64, i32, i32, i32]
+            lib.paged_attention_workspace_bytes.restype = sz
+            for fn in (lib.topk_beam, lib.topk_beam_bf16):
+                fn.argtypes = [p, p, i64, i32, i64, i32, p, p, p, p, sz, p]
+                fn.restype = i32
+            lib.topk_beam_workspace_bytes.argtypes = [i64, i32, i64, i32]
+            lib.topk_beam_workspace_bytes.restype = sz
+            lib.beam_reorder.argtypes = [p, p, p, i32, i64, i32, i32, p, p]
+            lib.beam_reorder.restype = i32
             lib.topk_status_string.argtypes = [i32]
             lib.topk_status_string.restype = ctypes.c_char_p
             lib.topk_device_status.argtypes = [ctypes.POINTER(ctypes.c_int)]

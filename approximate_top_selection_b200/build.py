@@ -2,21 +2,25 @@
 
     python -m approximate_top_selection_b200.build [--force]
 
-Produces approximate_top_selection_b200/libtopk_b200.so from csrc/topk_api.cu
-(one translation unit that includes every kernel).
+Produces approximate_top_selection_b200/libtopk_b200.so from two translation
+units, csrc/topk_api.cu (the selections) and csrc/decode_api.cu (cache,
+attention and beam search), compiled side by side; a unit is compiled again
+only when a file it includes is newer than its object.
 """
 from __future__ import annotations
 
 import glob
 import os
+import re
 import shutil
 import subprocess
 import sys
+import time
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 LIB = os.path.join(PKG, "libtopk_b200.so")
-MAIN = os.path.join(PKG, "csrc", "topk_api.cu")
+UNITS = [os.path.join(PKG, "csrc", "topk_api.cu"), os.path.join(PKG, "csrc", "decode_api.cu")]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 
 
@@ -39,15 +43,47 @@ def stale() -> bool:
     return any(os.path.getmtime(s) > t for s in sources())
 
 
+def _includes(path: str, seen=None) -> set:
+    """`path` and the files it includes by a quoted name, all the way down."""
+    seen = set() if seen is None else seen
+    path = os.path.normpath(path)
+    if path not in seen:
+        seen.add(path)
+        with open(path) as f:
+            for name in re.findall(r'^#include "([^"]+)"', f.read(), flags=re.M):
+                _includes(os.path.join(os.path.dirname(path), name), seen)
+    return seen
+
+
+def _object(unit: str) -> str:
+    return os.path.splitext(unit)[0] + ".o"
+
+
+def _object_stale(unit: str) -> bool:
+    obj = _object(unit)
+    return not os.path.exists(obj) or any(os.path.getmtime(s) > os.path.getmtime(obj) for s in _includes(unit))
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
     if not force and not stale():
         return LIB
-    tmp = LIB + ".tmp%d" % os.getpid()
-    cmd = [_nvcc(), "-std=c++17", "-O3", "-lineinfo", *ARCH, "-Xcompiler", "-fPIC", "-shared",
-           "-o", tmp, MAIN]
+    flags = ["-std=c++17", "-O3", "-lineinfo", *ARCH, "-Xcompiler", "-fPIC"]
     if verbose:
-        cmd.insert(1, "-Xptxas=-v")
-    subprocess.check_call(cmd)
+        flags.insert(0, "-Xptxas=-v")
+    running = []
+    began = time.time()  # an object is as old as the sources it was started from
+    for unit in UNITS:
+        if force or _object_stale(unit):
+            tmp = _object(unit) + ".tmp%d" % os.getpid()
+            running.append((subprocess.Popen([_nvcc(), *flags, "-c", "-o", tmp, unit]), tmp, _object(unit)))
+    failed = [p.args for p, _, _ in running if p.wait() != 0]
+    if failed:
+        raise subprocess.CalledProcessError(1, failed[0])
+    for _, tmp, obj in running:
+        os.utime(tmp, (began, began))
+        os.replace(tmp, obj)
+    tmp = LIB + ".tmp%d" % os.getpid()
+    subprocess.check_call([_nvcc(), *ARCH, "-shared", "-o", tmp, *[_object(u) for u in UNITS]])
     os.replace(tmp, LIB)
     return LIB
 

@@ -1,0 +1,295 @@
+// decode_api.cu -- C ABI of the operators of a decoding step around the
+// selections: the paged cache, attention over it, and beam search.  A
+// translation unit of its own, compiled next to topk_api.cu.
+
+// common.cuh defines the status word and the self-test kernel with external
+// linkage for topk_api.cu; in this unit they get names of their own.
+#define g_device_status g_decode_device_status
+#define wait_timeout_probe decode_wait_timeout_probe
+
+#include <algorithm>
+#include <cmath>
+
+#include "beam.cuh"
+#include "kv_cache.cuh"
+#include "launch.cuh"
+#include "paged_attention.cuh"
+
+namespace tk {
+
+namespace {
+
+constexpr int kMaxReorder = 256;
+constexpr int64_t kMaxGridX = 2147483647LL;
+
+bool cache_head_dim(int d) { return d == 64 || d == 128 || d == 256; }
+
+// Checks a cache description and builds the device view.
+int cache_view(const topk_cache* c, CacheView* v) {
+  if (!c || !c->data) return TOPK_EINVAL;
+  if (c->pages < 1 || c->kv_heads < 1 || c->page_size < 1 || c->d < 1) return TOPK_EINVAL;
+  if (c->type != TOPK_CACHE_BF16 && c->type != TOPK_CACHE_E4M3) return TOPK_EINVAL;
+  if (!cache_head_dim(c->d)) return TOPK_EUNSUPPORTED;
+  if (c->pages > kMaxN) return TOPK_EUNSUPPORTED;  // page numbers are int32
+  const int64_t esz = c->type == TOPK_CACHE_BF16 ? 2 : 1;
+  if (!aligned16(c->data)) return TOPK_EINVAL;
+  const int64_t strides[3] = {c->page_stride, c->head_stride, c->token_stride};
+  for (int64_t s : strides)
+    if (s < 0 || s > kMaxElems || (s * esz) % 16 != 0) return TOPK_EINVAL;
+  if (c->type == TOPK_CACHE_E4M3) {
+    if (!c->scale || (reinterpret_cast<uintptr_t>(c->scale) & 3u)) return TOPK_EINVAL;
+    const int64_t ss[3] = {c->scale_page_stride, c->scale_head_stride, c->scale_token_stride};
+    for (int64_t s : ss)
+      if (s < 0 || s > kMaxElems) return TOPK_EINVAL;
+  }
+  v->data = static_cast<unsigned char*>(c->data);
+  v->scale = c->type == TOPK_CACHE_E4M3 ? c->scale : nullptr;
+  v->page_stride = c->page_stride * esz;
+  v->head_stride = c->head_stride * esz;
+  v->token_stride = c->token_stride * esz;
+  v->s_page_stride = c->scale_page_stride;
+  v->s_head_stride = c->scale_head_stride;
+  v->s_token_stride = c->scale_token_stride;
+  v->pages = c->pages;
+  v->kv_heads = c->kv_heads;
+  v->page_size = c->page_size;
+  return TOPK_OK;
+}
+
+bool same_shape(const topk_cache* a, const topk_cache* b) {
+  return a->pages == b->pages && a->kv_heads == b->kv_heads && a->page_size == b->page_size && a->d == b->d &&
+         a->type == b->type;
+}
+
+int table_view(const int32_t* table, int64_t stride, int width, const int32_t* lens, int64_t batch, int page_size,
+               TableView* t) {
+  if (!table || !lens) return TOPK_EINVAL;
+  if (batch < 1 || width < 1 || stride < 0 || stride > kMaxElems) return TOPK_EINVAL;
+  if (batch > kMaxN) return TOPK_EUNSUPPORTED;
+  t->table = table;
+  t->lens = lens;
+  t->stride = stride;
+  t->capacity = std::min(static_cast<int64_t>(width) * page_size, kMaxN);
+  t->batch = static_cast<int>(batch);
+  return TOPK_OK;
+}
+
+template <int D, bool kE4m3>
+int launch_attend(const AttendArgs& a, const DeviceInfo& dev, cudaStream_t st) {
+  (void)dev;
+  int rc = prepare_kernel(paged_attention_simple<D, kE4m3>);
+  if (rc) return rc;
+  const int64_t rows = static_cast<int64_t>(a.tab.batch) * a.heads;
+  if (rows > kMaxGridX) return TOPK_EUNSUPPORTED;
+  return launch_pdl(paged_attention_simple<D, kE4m3>, dim3(static_cast<unsigned>(rows)), dim3(128), 0, st, a);
+}
+
+template <int D, bool kE4m3>
+int launch_write(const WriteArgs& a, const DeviceInfo& dev, cudaStream_t st) {
+  int rc = prepare_kernel(cache_write_kernel<D, kE4m3>);
+  if (rc) return rc;
+  const int64_t rows = a.tokens * a.cache[0].kv_heads * 2;
+  const int64_t per = 256 / (D / 8);
+  const int64_t grid = std::min((rows + per - 1) / per, static_cast<int64_t>(dev.sms) * 8);
+  return launch_pdl(cache_write_kernel<D, kE4m3>, dim3(static_cast<unsigned>(grid)), dim3(256), 0, st, a);
+}
+
+template <int D, bool kE4m3>
+int launch_read(const ReadArgs& a, const DeviceInfo& dev, cudaStream_t st) {
+  int rc = prepare_kernel(cache_read_kernel<D, kE4m3>);
+  if (rc) return rc;
+  const int64_t rows = static_cast<int64_t>(a.tab.batch) * a.cache.kv_heads * a.n;
+  const int64_t per = 256 / (D / 8);
+  const int64_t grid = std::min((rows + per - 1) / per, static_cast<int64_t>(dev.sms) * 8);
+  return launch_pdl(cache_read_kernel<D, kE4m3>, dim3(static_cast<unsigned>(grid)), dim3(256), 0, st, a);
+}
+
+// Picks the instantiation for (d, cache type).
+#define TK_BY_CACHE(fn, d, e4m3, ...)                                          \
+  ((d) == 64    ? ((e4m3) ? fn<64, true>(__VA_ARGS__) : fn<64, false>(__VA_ARGS__))   \
+   : (d) == 128 ? ((e4m3) ? fn<128, true>(__VA_ARGS__) : fn<128, false>(__VA_ARGS__)) \
+                : ((e4m3) ? fn<256, true>(__VA_ARGS__) : fn<256, false>(__VA_ARGS__)))
+
+template <typename T>
+int run_beam(const T* logits, const float* scores, int64_t batch, int beams, int64_t n, int k, float* out_scores,
+             int32_t* out_parent, int32_t* out_token, void* ws, size_t ws_bytes, void* stream) {
+  (void)ws;
+  (void)ws_bytes;
+  if (!logits || !scores || !out_scores || !out_parent || !out_token) return TOPK_EINVAL;
+  if (batch < 1 || beams < 1 || n < 1 || k < 1 || n > kMaxN) return TOPK_EINVAL;
+  if (beams > TOPK_BEAM_MAX || k > TOPK_BEAM_MAX) return TOPK_EUNSUPPORTED;
+  if (batch > kMaxElems / beams / n || batch > kMaxGridX) return TOPK_EUNSUPPORTED;
+  int rc = prepare_kernel(topk_beam_simple<T>);
+  if (rc) return rc;
+  const BeamArgs a{logits, scores, n, beams, k, out_scores, out_parent, out_token};
+  return launch_pdl(topk_beam_simple<T>, dim3(static_cast<unsigned>(batch)), dim3(kBeamThreads), 0,
+                    static_cast<cudaStream_t>(stream), a);
+}
+
+}  // namespace
+
+int decode_take_device_status(int* out) { return take_device_status(out); }
+
+}  // namespace tk
+
+using namespace tk;
+
+extern "C" {
+
+size_t paged_attention_workspace_bytes(int64_t batch, int heads, int lists, int d) {
+  (void)batch;
+  (void)heads;
+  (void)lists;
+  (void)d;
+  return 0;
+}
+
+int paged_attention(const uint16_t* q, int64_t q_stride, int64_t batch, int heads, const topk_cache* k_cache,
+                    const topk_cache* v_cache, const int32_t* block_table, int64_t table_stride, int table_width,
+                    const int32_t* seq_lens, const int32_t* positions, int lists, int c, float scale, uint16_t* out,
+                    float* out_lse, void* workspace, size_t workspace_bytes, void* stream) {
+  (void)workspace;
+  (void)workspace_bytes;
+  if (!q || !out) return TOPK_EINVAL;
+  AttendArgs a{};
+  int rc;
+  if ((rc = cache_view(k_cache, &a.k)) || (rc = cache_view(v_cache, &a.v))) return rc;
+  if (!same_shape(k_cache, v_cache)) return TOPK_EINVAL;
+  if ((rc = table_view(block_table, table_stride, table_width, seq_lens, batch, k_cache->page_size, &a.tab)))
+    return rc;
+  if (heads < 1 || heads % k_cache->kv_heads) return TOPK_EINVAL;
+  if (!std::isfinite(scale)) return TOPK_EINVAL;
+  if (!aligned16(q) || !aligned16(out) || q_stride < 0 || q_stride > kMaxElems || q_stride % 8) return TOPK_EINVAL;
+  if (positions) {
+    if (lists < 1 || c < 1 || lists % k_cache->kv_heads || heads % lists) return TOPK_EINVAL;
+    if (c > kMaxElems / lists / batch) return TOPK_EUNSUPPORTED;
+  } else if (lists != 0 || c != 0) {
+    return TOPK_EINVAL;
+  }
+  if (batch > kMaxN / heads) return TOPK_EUNSUPPORTED;
+  DeviceInfo dev;
+  if ((rc = current_device_info(&dev))) return rc;
+  a.q = q;
+  a.q_stride = q_stride;
+  a.positions = positions;
+  a.heads = heads;
+  a.lists = positions ? lists : k_cache->kv_heads;
+  a.c = c;
+  a.scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
+  a.out = out;
+  a.lse = out_lse;
+  return TK_BY_CACHE(launch_attend, k_cache->d, a.k.scale != nullptr, a, dev, static_cast<cudaStream_t>(stream));
+}
+
+int cache_write(const uint16_t* k, int64_t k_token_stride, int64_t k_head_stride, const uint16_t* v,
+                int64_t v_token_stride, int64_t v_head_stride, int64_t tokens, const topk_cache* k_cache,
+                const topk_cache* v_cache, const int64_t* slots, void* stream) {
+  if (!k || !v || !slots) return TOPK_EINVAL;
+  WriteArgs a{};
+  int rc;
+  if ((rc = cache_view(k_cache, &a.cache[0])) || (rc = cache_view(v_cache, &a.cache[1]))) return rc;
+  if (!same_shape(k_cache, v_cache)) return TOPK_EINVAL;
+  if (tokens < 1) return TOPK_EINVAL;
+  if (tokens > kMaxElems / k_cache->kv_heads / k_cache->d) return TOPK_EUNSUPPORTED;
+  if (!aligned16(k) || !aligned16(v)) return TOPK_EINVAL;
+  const int64_t strides[4] = {k_token_stride, k_head_stride, v_token_stride, v_head_stride};
+  for (int64_t s : strides)
+    if (s < 0 || s > kMaxElems || s % 8) return TOPK_EINVAL;
+  DeviceInfo dev;
+  if ((rc = current_device_info(&dev))) return rc;
+  a.src[0] = k;
+  a.src[1] = v;
+  a.token_stride[0] = k_token_stride;
+  a.token_stride[1] = v_token_stride;
+  a.head_stride[0] = k_head_stride;
+  a.head_stride[1] = v_head_stride;
+  a.slots = slots;
+  a.tokens = tokens;
+  return TK_BY_CACHE(launch_write, k_cache->d, a.cache[0].scale != nullptr, a, dev, static_cast<cudaStream_t>(stream));
+}
+
+int cache_read(const topk_cache* cache, const int32_t* block_table, int64_t table_stride, int table_width,
+               const int32_t* seq_lens, int64_t batch, int64_t n, uint16_t* out, void* stream) {
+  ReadArgs a{};
+  int rc;
+  if (!out || n < 1 || n > kMaxN) return TOPK_EINVAL;
+  if ((rc = cache_view(cache, &a.cache))) return rc;
+  if ((rc = table_view(block_table, table_stride, table_width, seq_lens, batch, cache->page_size, &a.tab))) return rc;
+  if (batch > kMaxElems / cache->kv_heads / n / cache->d) return TOPK_EUNSUPPORTED;
+  if (!aligned16(out)) return TOPK_EINVAL;
+  DeviceInfo dev;
+  if ((rc = current_device_info(&dev))) return rc;
+  a.n = n;
+  a.out = out;
+  return TK_BY_CACHE(launch_read, cache->d, a.cache.scale != nullptr, a, dev, static_cast<cudaStream_t>(stream));
+}
+
+size_t topk_beam_workspace_bytes(int64_t batch, int beams, int64_t n, int k) {
+  (void)batch;
+  (void)beams;
+  (void)n;
+  (void)k;
+  return 0;
+}
+
+int topk_beam(const float* logits, const float* beam_scores, int64_t batch, int beams, int64_t n, int k,
+              float* out_scores, int32_t* out_parent, int32_t* out_token, void* workspace, size_t workspace_bytes,
+              void* stream) {
+  return run_beam<float>(logits, beam_scores, batch, beams, n, k, out_scores, out_parent, out_token, workspace,
+                         workspace_bytes, stream);
+}
+
+int topk_beam_bf16(const uint16_t* logits, const float* beam_scores, int64_t batch, int beams, int64_t n, int k,
+                   float* out_scores, int32_t* out_parent, int32_t* out_token, void* workspace,
+                   size_t workspace_bytes, void* stream) {
+  return run_beam<uint16_t>(logits, beam_scores, batch, beams, n, k, out_scores, out_parent, out_token, workspace,
+                            workspace_bytes, stream);
+}
+
+int beam_reorder(const void* const* src, void* const* dst, const int64_t* row_bytes, int count, int64_t batch,
+                 int beams, int k, const int32_t* parents, void* stream) {
+  if (!src || !dst || !row_bytes || !parents) return TOPK_EINVAL;
+  if (count < 1 || batch < 1 || beams < 1 || k < 1) return TOPK_EINVAL;
+  if (count > kMaxReorder || batch > kMaxN / k || batch > kMaxN / beams) return TOPK_EUNSUPPORTED;
+  // No destination may overlap a source or another destination.
+  struct Span {
+    uintptr_t begin, end;
+    bool dst;
+  };
+  Span span[2 * kMaxReorder];
+  for (int i = 0; i < count; ++i) {
+    if (!src[i] || !dst[i] || row_bytes[i] < 1) return TOPK_EINVAL;
+    if (row_bytes[i] > kMaxElems / batch / std::max(beams, k)) return TOPK_EUNSUPPORTED;
+    const uintptr_t s = reinterpret_cast<uintptr_t>(src[i]), d = reinterpret_cast<uintptr_t>(dst[i]);
+    span[2 * i] = Span{s, s + static_cast<uintptr_t>(batch * beams * row_bytes[i]), false};
+    span[2 * i + 1] = Span{d, d + static_cast<uintptr_t>(batch * k * row_bytes[i]), true};
+  }
+  std::sort(span, span + 2 * count, [](const Span& a, const Span& b) { return a.begin < b.begin; });
+  uintptr_t any_end = 0, dst_end = 0;
+  for (int i = 0; i < 2 * count; ++i) {
+    if (span[i].begin < (span[i].dst ? any_end : dst_end)) return TOPK_EINVAL;
+    any_end = std::max(any_end, span[i].end);
+    if (span[i].dst) dst_end = std::max(dst_end, span[i].end);
+  }
+  int rc = prepare_kernel(beam_reorder_simple);
+  if (rc) return rc;
+  for (int first = 0; first < count; first += kReorderStates) {
+    ReorderArgs a{};
+    const int m = std::min(kReorderStates, count - first);
+    for (int i = 0; i < m; ++i) {
+      a.src[i] = static_cast<const unsigned char*>(src[first + i]);
+      a.dst[i] = static_cast<unsigned char*>(dst[first + i]);
+      a.row_bytes[i] = row_bytes[first + i];
+    }
+    a.parents = parents;
+    a.batch = batch;
+    a.beams = beams;
+    a.k = k;
+    rc = launch_pdl(beam_reorder_simple, dim3(static_cast<unsigned>(batch * k), static_cast<unsigned>(m)), dim3(256),
+                    0, static_cast<cudaStream_t>(stream), a);
+    if (rc) return rc;
+  }
+  return TOPK_OK;
+}
+
+}  // extern "C"

@@ -234,6 +234,159 @@ int score_topk(const uint16_t *q_dev, int64_t rows, int d, const uint16_t *K_dev
 int topk_bucketed_noalloc(const float *scores_dev, int64_t rows, int64_t n, int k, int b, int kb,
                           float *out_vals_dev, int32_t *out_idx_dev, void *stream);
 
+/* ------------------------------------------------------------------------
+ * The decoding step around the selections.  The pages leave these parts to
+ * the model that calls the selector: the key-value cache that the decode
+ * selector scores, the attention over the cache or over the selected
+ * positions, and beam search over the vocabulary next to sampling.
+ * ------------------------------------------------------------------------ */
+
+#define TOPK_CACHE_BF16 0 /* rows of bf16 values */
+#define TOPK_CACHE_E4M3 1 /* rows of 8-bit codes (4 exponent bits, 3 mantissa bits) and a float32 scale */
+
+/* One paged cache tensor (the keys, or the values) in device memory:
+ * element [page][head][offset][i], i < d contiguous, the other three with any
+ * strides.  Token t of a sequence whose row of the block table is T lies on
+ * page T[t / page_size] at offset t % page_size; pages are given out by the
+ * caller.  With page_size = n and one page per sequence a contiguous
+ * [batch][kv_heads][n][d] cache, as score_topk reads it, is such a tensor.
+ * d is 64, 128 or 256 (else TOPK_EUNSUPPORTED); data is 16-byte aligned and
+ * every stride a multiple of 16 bytes.  An E4M3 row (page, head, offset) with
+ * scale s holds the values code_i * s; scales are read as any floats, and
+ * cache_write writes powers of two. */
+typedef struct {
+    void *data;
+    float *scale;            /* E4M3: [pages][kv_heads][page_size] with the strides below; else ignored */
+    int64_t pages;           /* pages of the tensor, < 2^31 */
+    int kv_heads;
+    int page_size;           /* tokens per page, any number >= 1 */
+    int d;
+    int type;                /* TOPK_CACHE_BF16 or TOPK_CACHE_E4M3 */
+    int64_t page_stride, head_stride, token_stride;                   /* elements of data */
+    int64_t scale_page_stride, scale_head_stride, scale_token_stride; /* elements of scale */
+} topk_cache;
+
+/* Writes the keys and values of new tokens into their slots.
+ *   k_dev, v_dev  bf16; row (token, head) starts at token * *_token_stride +
+ *                 head * *_head_stride elements and holds d values; 16-byte
+ *                 aligned, strides multiples of 8 elements.
+ *   slots_dev     [tokens] int64: page * page_size + offset.  A negative slot
+ *                 is skipped (padding); one behind the last page is skipped
+ *                 and sets TOPK_DEV_BAD_INDEX.  The slots of one call must be
+ *                 distinct (a repeated one ends up holding either row, or a
+ *                 mix of both).
+ *   k_cache, v_cache  of the same shape and type (host structures).
+ * BF16 rows are copied.  An E4M3 row x becomes code_i = x_i / 2^e rounded to
+ * nearest even and scale 2^e, with the smallest e >= -127 for which max|x_i|
+ * <= 448 * 2^e (e = 0 for a row of zeros): the values read back are within
+ * 2^-4 of x_i relatively, or within 2^(e-10) where that is more.  A row that
+ * holds a NaN or an infinity reads back as NaN throughout.  Other slots are
+ * left as they were.  Asynchronous on `stream`; no workspace. */
+int cache_write(const uint16_t *k_dev, int64_t k_token_stride, int64_t k_head_stride,
+                const uint16_t *v_dev, int64_t v_token_stride, int64_t v_head_stride,
+                int64_t tokens, const topk_cache *k_cache, const topk_cache *v_cache,
+                const int64_t *slots_dev, void *stream);
+
+/* Reads the first n tokens of every sequence back as contiguous bf16 rows:
+ * out[b][h][t] for t < min(n, seq_lens[b]), zeros behind.  With batch *
+ * kv_heads rows of [n x d] keys this is what score_topk and score_rerank take.
+ * An E4M3 value is code * scale rounded once to bf16 (exact for the scales of
+ * cache_write).
+ *   block_table_dev  [batch] rows of table_width int32 page numbers, row b at
+ *                    b * table_stride.  Entries behind a sequence's last page
+ *                    are not read; a page that does not exist reads as zeros
+ *                    and sets TOPK_DEV_BAD_INDEX.
+ *   seq_lens_dev     [batch] int32; a negative length is 0, one above
+ *                    table_width * page_size is held to that and sets
+ *                    TOPK_DEV_BAD_INDEX.
+ *   out_dev          [batch x kv_heads x n x d] bf16, 16-byte aligned. */
+int cache_read(const topk_cache *cache, const int32_t *block_table_dev, int64_t table_stride,
+               int table_width, const int32_t *seq_lens_dev, int64_t batch, int64_t n,
+               uint16_t *out_dev, void *stream);
+
+/* Attention of one new token per sequence: out[b][h] = sum_j p_j V_j with
+ * p = softmax over j of scale * q[b][h] . K_j, and lse[b][h] = log sum_j
+ * exp(scale * q[b][h] . K_j), over the tokens j < seq_lens[b], or over the
+ * listed positions.  Query head h reads key-value head h / (heads / kv_heads).
+ * Products, sums and softmax are float32; out is rounded once to bf16.
+ *   q_dev         bf16, sequence b at b * q_stride elements, [heads x d]
+ *                 contiguous there; 16-byte aligned, q_stride a multiple of 8.
+ *   heads         a multiple of kv_heads.
+ *   block_table_dev, table_stride, table_width, seq_lens_dev  as in
+ *                 cache_read.  A token whose page does not exist is left out
+ *                 and sets TOPK_DEV_BAD_INDEX.
+ *   positions_dev NULL for the whole sequence (lists = c = 0), else int32
+ *                 [batch x lists x c]: list l serves the query heads h with
+ *                 h / (heads / lists) = l; lists is a multiple of kv_heads
+ *                 that divides heads.  These are the indices score_topk or
+ *                 score_rerank return.  A negative position is an empty slot,
+ *                 one at or behind seq_lens[b] is left out (at or behind
+ *                 table_width * page_size it also sets TOPK_DEV_BAD_INDEX);
+ *                 a position listed twice counts twice.
+ *   out_dev       [batch x heads x d] bf16; out_lse_dev NULL or [batch x
+ *                 heads] float32.
+ * A head with no token to attend to, or whose scores are all -inf, gives
+ * zeros and an lse of -inf.
+ * The workspace holds paged_attention_workspace_bytes(...) bytes, 16-byte
+ * aligned, zero-filled before its first use; a call leaves it ready for any
+ * later call of this operator or of topk_beam (not of the selections above),
+ * and calls that overlap on the GPU must not share one. */
+int paged_attention(const uint16_t *q_dev, int64_t q_stride, int64_t batch, int heads,
+                    const topk_cache *k_cache, const topk_cache *v_cache,
+                    const int32_t *block_table_dev, int64_t table_stride, int table_width,
+                    const int32_t *seq_lens_dev, const int32_t *positions_dev, int lists, int c,
+                    float scale, uint16_t *out_dev, float *out_lse_dev, void *workspace_dev,
+                    size_t workspace_bytes, void *stream);
+
+/* Bytes of workspace of a paged_attention call on the current device (lists =
+ * 0 without positions); 0 for invalid sizes. */
+size_t paged_attention_workspace_bytes(int64_t batch, int heads, int lists, int d);
+
+#define TOPK_BEAM_MAX 128 /* largest number of beams, and of continuations kept, per sentence */
+
+/* One step of beam search: the k best continuations of every sentence's beams.
+ * Continuation (i, t) is worth s_i + x_it - log sum_t' exp(x_it').
+ *   logits_dev      [batch x beams x n] float32.
+ *   beam_scores_dev [batch x beams] float32 s_i; -inf marks a beam that has
+ *                   ended or does not exist yet: its logits are not looked at.
+ *   k               1 <= k <= 128, beams <= 128 (else TOPK_EUNSUPPORTED); twice
+ *                   the beams leaves enough when every beam may end.
+ *   out_scores_dev  [batch x k] float32 values, best first; out_parent_dev
+ *                   [batch x k] int32 beams; out_token_dev [batch x k] int32.
+ * Continuations rank by value, compared in 64 bits (NaN first), then by lower
+ * beam, larger logit, lower token.  A logit of -inf gives no continuation; a
+ * beam whose logits hold a NaN or +inf has the value NaN for all of its own.
+ * When there are fewer than k, the remaining slots hold -inf, -1, -1.
+ * Workspace: topk_beam_workspace_bytes(...), shared with paged_attention on
+ * the terms given there. */
+int topk_beam(const float *logits_dev, const float *beam_scores_dev, int64_t batch, int beams,
+              int64_t n, int k, float *out_scores_dev, int32_t *out_parent_dev,
+              int32_t *out_token_dev, void *workspace_dev, size_t workspace_bytes, void *stream);
+
+/* topk_beam on bfloat16 logits (raw 16-bit patterns, widened exactly). */
+int topk_beam_bf16(const uint16_t *logits_dev, const float *beam_scores_dev, int64_t batch,
+                   int beams, int64_t n, int k, float *out_scores_dev, int32_t *out_parent_dev,
+                   int32_t *out_token_dev, void *workspace_dev, size_t workspace_bytes,
+                   void *stream);
+
+/* Bytes of workspace of a topk_beam or topk_beam_bf16 call on the current
+ * device; 0 for invalid sizes. */
+size_t topk_beam_workspace_bytes(int64_t batch, int beams, int64_t n, int k);
+
+/* Brings per-beam states into the order topk_beam chose: for every tensor s
+ * and new beam (b, j), row dst[s][b][j] = row src[s][b][parents[b][j]].  A
+ * parent of -1 (a slot topk_beam left empty) gives a row of zeros; any other
+ * parent outside [0, beams) does too and sets TOPK_DEV_BAD_INDEX.
+ *   src, dst     HOST arrays of `count` device pointers, 1 <= count <= 256
+ *                (else TOPK_EUNSUPPORTED); any alignment.
+ *   row_bytes    HOST array [count]: bytes of one beam's row, contiguous; src[s]
+ *                holds batch * beams rows, dst[s] batch * k.
+ *   parents_dev  [batch x k] int32.
+ * A destination that overlaps a source or another destination is refused
+ * (TOPK_EINVAL).  Asynchronous on `stream`; no workspace. */
+int beam_reorder(const void *const *src, void *const *dst, const int64_t *row_bytes, int count,
+                 int64_t batch, int beams, int k, const int32_t *parents_dev, void *stream);
+
 /* Self-test of the bounded waits (no counterpart in the paper): one thread
  * waits, for at most limit_ns nanoseconds (1e3 .. 2e9, else TOPK_EINVAL), on
  * a barrier that nothing completes, gives up and records TOPK_DEV_WAIT_TIMEOUT
@@ -252,7 +405,8 @@ const char *topk_status_string(int status);
 int topk_device_status(int *status_out);
 
 #define TOPK_DEV_WAIT_TIMEOUT 1 /* a bulk-copy wait in a streaming kernel expired */
-#define TOPK_DEV_BAD_INDEX 2    /* topk_bucketed_merge or score_rerank skipped an index out of range */
+#define TOPK_DEV_BAD_INDEX 2    /* an index out of range (of a candidate, position, slot, page, length or
+                                beam) was skipped; see each call */
 #define TOPK_DEV_DRAIN_TIMEOUT 4 /* after an expired wait, the kernel's wait for its own bulk copies
                                     still in flight expired too: the kernel returned while a copy
                                     may still have been writing to its shared memory, so the
