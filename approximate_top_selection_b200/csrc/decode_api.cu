@@ -74,14 +74,36 @@ int table_view(const int32_t* table, int64_t stride, int width, const int32_t* l
   return TOPK_OK;
 }
 
+// CTAs of the attention's line: all that are resident at once.  The workspace
+// is sized for two per SM, the most any instantiation has.
+constexpr int kAttendCtasPerSm = 2;
+
+size_t attend_workspace(int d, const DeviceInfo& dev) {
+  const int ctas = std::min(dev.sms * kAttendCtasPerSm, kAttendMaxCtas);
+  return kAttendTicketBytes + static_cast<size_t>(ctas) * 2 * attend_part_floats(d) * 4;
+}
+
+template <int D, bool kE4m3, bool kFull>
+int launch_attend_rows(AttendArgs& a, const DeviceInfo& dev, cudaStream_t st) {
+  using S = AttendShape<D, kE4m3>;
+  if (S::kSmem > dev.max_smem_optin) return TOPK_EUNSUPPORTED;
+  int rc, per_sm = 0;
+  if ((rc = occupancy(paged_attention_kernel<D, kE4m3, kFull>, kAttendThreads, S::kSmem, &per_sm))) return rc;
+  const int64_t most = a.positions ? a.c : a.tab.capacity;
+  const int64_t granules = (most + S::kGranule - 1) / S::kGranule;
+  const int64_t units = static_cast<int64_t>(a.lists) * a.row_tiles * a.tab.batch;
+  int64_t ctas = std::min(std::min(per_sm, kAttendCtasPerSm) * dev.sms, kAttendMaxCtas);
+  if (granules <= ctas / units) ctas = std::max<int64_t>(1, granules * units);
+  return launch_pdl(paged_attention_kernel<D, kE4m3, kFull>, dim3(static_cast<unsigned>(ctas)), dim3(kAttendThreads),
+                    S::kSmem, st, a);
+}
+
 template <int D, bool kE4m3>
-int launch_attend(const AttendArgs& a, const DeviceInfo& dev, cudaStream_t st) {
-  (void)dev;
-  int rc = prepare_kernel(paged_attention_simple<D, kE4m3>);
-  if (rc) return rc;
-  const int64_t rows = static_cast<int64_t>(a.tab.batch) * a.heads;
-  if (rows > kMaxGridX) return TOPK_EUNSUPPORTED;
-  return launch_pdl(paged_attention_simple<D, kE4m3>, dim3(static_cast<unsigned>(rows)), dim3(128), 0, st, a);
+int launch_attend(AttendArgs& a, const DeviceInfo& dev, cudaStream_t st) {
+  const int group = a.heads / a.lists;
+  a.row_tiles = (group + 15) / 16;
+  if (static_cast<int64_t>(a.lists) * a.row_tiles > kMaxN / a.tab.batch) return TOPK_EUNSUPPORTED;
+  return group > 8 ? launch_attend_rows<D, kE4m3, true>(a, dev, st) : launch_attend_rows<D, kE4m3, false>(a, dev, st);
 }
 
 template <int D, bool kE4m3>
@@ -137,19 +159,15 @@ using namespace tk;
 extern "C" {
 
 size_t paged_attention_workspace_bytes(int64_t batch, int heads, int lists, int d) {
-  (void)batch;
-  (void)heads;
-  (void)lists;
-  (void)d;
-  return 0;
+  DeviceInfo dev;
+  if (batch < 1 || heads < 1 || lists < 0 || !cache_head_dim(d) || current_device_info(&dev)) return 0;
+  return attend_workspace(d, dev);
 }
 
 int paged_attention(const uint16_t* q, int64_t q_stride, int64_t batch, int heads, const topk_cache* k_cache,
                     const topk_cache* v_cache, const int32_t* block_table, int64_t table_stride, int table_width,
                     const int32_t* seq_lens, const int32_t* positions, int lists, int c, float scale, uint16_t* out,
                     float* out_lse, void* workspace, size_t workspace_bytes, void* stream) {
-  (void)workspace;
-  (void)workspace_bytes;
   if (!q || !out) return TOPK_EINVAL;
   AttendArgs a{};
   int rc;
@@ -169,6 +187,12 @@ int paged_attention(const uint16_t* q, int64_t q_stride, int64_t batch, int head
   if (batch > kMaxN / heads) return TOPK_EUNSUPPORTED;
   DeviceInfo dev;
   if ((rc = current_device_info(&dev))) return rc;
+  if (!workspace || workspace_bytes < attend_workspace(k_cache->d, dev)) return TOPK_EWORKSPACE;
+  if (!aligned16(workspace)) return TOPK_EINVAL;
+  a.tickets = static_cast<uint32_t*>(workspace);
+  a.parts = reinterpret_cast<float*>(static_cast<unsigned char*>(workspace) + kAttendTicketBytes);
+  a.same_strides = a.k.page_stride == a.v.page_stride && a.k.head_stride == a.v.head_stride &&
+                   a.k.token_stride == a.v.token_stride;
   a.q = q;
   a.q_stride = q_stride;
   a.positions = positions;
