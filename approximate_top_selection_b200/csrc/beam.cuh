@@ -39,132 +39,525 @@ __device__ __forceinline__ bool ranks_above(const Cont& a, const Cont& b) {
   return a.token < b.token;
 }
 
+// Two levels, one launch.  A CTA takes a piece of a beam's row, at most 64 KB
+// that stay in its registers: the piece's maximum, its sum of exponentials and
+// its k largest logits.  The CTA of a sentence that finishes last (an atomic
+// ticket, nobody waits) turns the sums into lse_i and picks the k best of all
+// pieces' lists.  Within a beam the order is the logits', so a piece's list
+// can be cut at k before lse_i is known.
+//
+// The k largest of a piece without sorting it: of the 256 threads' maxima, the
+// j-th largest of each warp (j = ceil(k / 8)) bounds the k-th largest value
+// from below in all; the few elements at or above the smallest of these bounds
+// are gathered while the exponentials are summed, and ranked by counting.
+// Where that leaves more than kBeamCap (equal logits), the bound is bisected,
+// over keys and then over indices.
+//
+// Bound by reading the logits.  A logit costs one exponential (16 per clock
+// and SM: 4.5e12 a second, against 1.6e12 fp32 or 3.2e12 bf16 logits a second
+// at full bandwidth) and about six other instructions.
 struct BeamArgs {
   const void* logits;   // [batch][beams][n]
   const float* scores;  // [batch][beams]
   int64_t n;
   int beams, k;
+  int pieces;           // per row
+  int64_t first;        // sentence of blockIdx.x = 0
   float* out_scores;    // [batch][k]
   int32_t* out_parent;  // [batch][k]
   int32_t* out_token;   // [batch][k]
+  uint32_t* tickets;    // [sentences of the launch], zero between calls
+  uint2* sums;          // [rows of the launch][pieces]: key of the maximum, sum of 2^((x - max) log2 e)
+  uint64_t* lists;      // [rows of the launch][pieces][k]
 };
 
 constexpr int kMaxBeams = 128;
+constexpr int kBeamCap = 512;       // gathered candidates; more than the largest k
+constexpr int kBeamVectors = 16;    // 16-byte vectors per thread
+constexpr int kBeamTickets = 4096;  // sentences per launch
 
-// One CTA per sentence: log-sum-exp of every beam, then k rounds that each
-// find the best continuation below the last one.
-template <typename T>
-__global__ void __launch_bounds__(kBeamThreads) topk_beam_simple(BeamArgs p) {
-  __shared__ double off[kMaxBeams];
-  __shared__ double rsum[kBeamThreads];
-  __shared__ float rmax[kBeamThreads];
-  __shared__ Cont best[kBeamThreads];
-  pdl_wait_then_release();
-  const int tid = threadIdx.x;
-  const int64_t b = blockIdx.x;
-  const float ninf = __int_as_float(0xff800000);
-  for (int i = 0; i < p.beams; ++i) {
-    const T* x = static_cast<const T*>(p.logits) + (b * p.beams + i) * p.n;
-    float m = ninf;
-    bool bad = false;
-    for (int64_t t = tid; t < p.n; t += kBeamThreads) {
-      const float v = logit_value(x[t]);
-      bad |= v != v || v == __int_as_float(0x7f800000);
-      m = fmaxf(m, v);
-    }
-    rmax[tid] = m;
-    bad = __syncthreads_or(bad);
-    for (int s = kBeamThreads / 2; s; s >>= 1) {
-      if (tid < s) rmax[tid] = fmaxf(rmax[tid], rmax[tid + s]);
-      __syncthreads();
-    }
-    m = rmax[0];
-    double sum = 0.0;
-    if (!bad && m != ninf)
-      for (int64_t t = tid; t < p.n; t += kBeamThreads)
-        sum += exp(static_cast<double>(logit_value(x[t])) - static_cast<double>(m));
-    rsum[tid] = sum;
-    __syncthreads();
-    for (int s = kBeamThreads / 2; s; s >>= 1) {
-      if (tid < s) rsum[tid] += rsum[tid + s];
-      __syncthreads();
-    }
-    if (tid == 0)
-      off[i] = static_cast<double>(p.scores[b * p.beams + i]) -
-               (bad ? __longlong_as_double(0x7ff8000000000000ll) : static_cast<double>(m) + log(rsum[0]));
-    __syncthreads();
+// Order key of a candidate logit; 0 for one that gives no continuation.
+__device__ __forceinline__ uint32_t beam_key(float x) {
+  return x == __int_as_float(0xff800000) ? 0u : order_key(x);
+}
+
+// A key that at least k of the CTA's elements reach, given every thread's
+// largest key (0: none).  warp_keys: 8 words.
+__device__ __forceinline__ uint32_t beam_bound(uint32_t mine, int k, uint32_t* warp_keys) {
+  constexpr int kWarps = kBeamThreads / 32;
+  const int rounds = (k + kWarps - 1) / kWarps;
+  uint32_t last = 0;
+  for (int i = 0; i < rounds; ++i) {
+    last = __reduce_max_sync(0xffffffffu, mine);
+    if (last == 0) break;
+    if (mine == last) mine = 0;
   }
-  Cont last = {~0ull, ~0ull, 0};
-  bool first = true;
-  for (int j = 0; j < p.k; ++j) {
-    Cont mine = {0, 0, 0};  // value 0: none
-    for (int i = 0; i < p.beams; ++i) {
-      if (p.scores[b * p.beams + i] == ninf) continue;
-      const T* x = static_cast<const T*>(p.logits) + (b * p.beams + i) * p.n;
-      for (int64_t t = tid; t < p.n; t += kBeamThreads) {
-        const float v = logit_value(x[t]);
-        if (v == ninf) continue;
-        const Cont c = {order_key64(off[i] + static_cast<double>(v)),
-                        (static_cast<uint64_t>(~static_cast<uint32_t>(i)) << 32) | order_key(v),
-                        static_cast<uint32_t>(t)};
-        if ((first || ranks_above(last, c)) && ranks_above(c, mine)) mine = c;
-      }
+  if ((threadIdx.x & 31) == 0) warp_keys[threadIdx.x >> 5] = last;
+  __syncthreads();
+  // k <= 8: the k-th largest of the eight warps' maxima; else the smallest.
+  const int want = min(k, kWarps);
+  uint32_t bound = 0;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) {
+    int above = 0;
+#pragma unroll
+    for (int v = 0; v < kWarps; ++v) above += warp_keys[v] > warp_keys[w] || (warp_keys[v] == warp_keys[w] && v < w);
+    if (above == want - 1) bound = warp_keys[w];
+  }
+  return bound;
+}
+
+__device__ __forceinline__ int block_total(int mine, int* slot) {
+  __syncthreads();
+  if (threadIdx.x == 0) *slot = 0;
+  __syncthreads();
+  mine = __reduce_add_sync(0xffffffffu, mine);
+  if ((threadIdx.x & 31) == 0 && mine) atomicAdd(slot, mine);
+  __syncthreads();
+  return *slot;
+}
+
+struct BeamShared {
+  union {
+    uint64_t gathered[kBeamCap];
+    struct {
+      uint64_t value[kBeamCap], rest[kBeamCap];
+      uint32_t token[kBeamCap];
+    } cont;
+  };
+  double off[kMaxBeams];
+  double part[kBeamThreads / 32];
+  Cont best[kBeamThreads / 32];
+  uint32_t warp_keys[kBeamThreads / 32];
+  int count, total, last;
+};
+
+// The piece of a row that a CTA takes, as 16-byte vectors on 16-byte addresses:
+// vector v of a thread holds the row's elements from index(v) on.  A vector
+// behind the piece, and elements outside the row, read as -inf.
+template <typename T>
+struct BeamPiece {
+  static constexpr int kPer = 16 / sizeof(T);  // elements per vector
+  static constexpr uint32_t kFill = sizeof(T) == 4 ? 0xff800000u : 0xff80ff80u;
+  const T* row;
+  int64_t n;
+  int64_t w0, w1;  // vectors of the piece
+  int mis;         // elements of the row's first vector that lie before the row
+
+  __device__ __forceinline__ BeamPiece(const T* row_, int64_t n_, int piece, int pieces) : row(row_), n(n_) {
+    mis = static_cast<int>((reinterpret_cast<uintptr_t>(row) / sizeof(T)) % kPer);
+    const int64_t vectors = (n + mis + kPer - 1) / kPer;
+    w0 = vectors * piece / pieces;
+    w1 = vectors * (piece + 1) / pieces;
+  }
+  __device__ __forceinline__ int64_t vector(int v) const { return w0 + v * kBeamThreads + threadIdx.x; }
+  __device__ __forceinline__ int64_t index(int v) const { return vector(v) * kPer - mis; }
+  __device__ __forceinline__ bool inside(int64_t w) const { return w * kPer >= mis && (w + 1) * kPer - mis <= n; }
+  __device__ __forceinline__ uint4 load(int v) const {
+    const int64_t w = vector(v);
+    uint4 x = make_uint4(kFill, kFill, kFill, kFill);
+    if (w < w1 && inside(w)) x = __ldcs(reinterpret_cast<const uint4*>(row - mis + w * kPer));
+    return x;
+  }
+  // The row's first or last vector, which may hold elements of its neighbours.
+  __device__ __forceinline__ bool ragged(int v) const { return vector(v) < w1 && !inside(vector(v)); }
+  __device__ __forceinline__ uint4 load_ragged(int v) const {
+    uint32_t word[4] = {kFill, kFill, kFill, kFill};
+#pragma unroll
+    for (int e = 0; e < kPer; ++e) {
+      const int64_t i = index(v) + e;
+      if (i < 0 || i >= n) continue;
+      if constexpr (sizeof(T) == 4)
+        word[e] = __float_as_uint(row[i]);
+      else
+        word[e / 2] = e & 1 ? (word[e / 2] & 0xffffu) | (static_cast<uint32_t>(row[i]) << 16)
+                            : (word[e / 2] & 0xffff0000u) | row[i];
     }
-    best[tid] = mine;
-    __syncthreads();
-    for (int s = kBeamThreads / 2; s; s >>= 1) {
-      if (tid < s && ranks_above(best[tid + s], best[tid])) best[tid] = best[tid + s];
+    return make_uint4(word[0], word[1], word[2], word[3]);
+  }
+  static __device__ __forceinline__ float value(const uint4& x, int e) {
+    const int i = e * static_cast<int>(sizeof(T)) / 4;
+    const uint32_t w = i == 0 ? x.x : i == 1 ? x.y : i == 2 ? x.z : x.w;
+    if constexpr (sizeof(T) == 4) return __uint_as_float(w);
+    return __uint_as_float(e & 1 ? w & 0xffff0000u : w << 16);
+  }
+};
+
+__device__ __forceinline__ void beam_push(BeamShared& sh, uint32_t key, int64_t i) {
+  const int at = atomicAdd(&sh.count, 1);
+  if (at < kBeamCap) sh.gathered[at] = pack(key, static_cast<uint32_t>(i));
+}
+
+// Exactly the k best of the piece into sh.gathered: the bound bisected over
+// keys (the largest that k elements reach), then over the indices of the
+// elements that equal it.  Reads the piece again for every step.
+template <typename T>
+__device__ __noinline__ void beam_bisect(BeamShared* shp, const T* row, int64_t n, int piece, int pieces, int k) {
+  BeamShared& sh = *shp;
+  const BeamPiece<T> p(row, n, piece, pieces);
+  auto each = [&](auto&& f) {
+#pragma unroll 1
+    for (int v = 0; v < kBeamVectors; ++v) {
+      const uint4 x = p.ragged(v) ? p.load_ragged(v) : p.load(v);
+#pragma unroll
+      for (int e = 0; e < p.kPer; ++e) f(beam_key(p.value(x, e)), p.index(v) + e);
+    }
+  };
+  uint32_t lo = 1, hi = 0xffffffffu;
+  while (lo < hi) {
+    const uint32_t mid = lo + ((hi - lo) >> 1) + 1;
+    int c = 0;
+    each([&](uint32_t key, int64_t) { c += key >= mid; });
+    if (block_total(c, &sh.total) >= k)
+      lo = mid;
+    else
+      hi = mid - 1;
+  }
+  int c = 0;
+  each([&](uint32_t key, int64_t) { c += key > lo; });
+  const int equal = k - block_total(c, &sh.total);
+  int64_t a = 0, b = n - 1;
+  while (a < b) {
+    const int64_t mid = (a + b) >> 1;
+    c = 0;
+    each([&](uint32_t key, int64_t i) { c += key == lo && i <= mid; });
+    if (block_total(c, &sh.total) >= equal)
+      b = mid;
+    else
+      a = mid + 1;
+  }
+  __syncthreads();
+  if (threadIdx.x == 0) sh.count = 0;
+  __syncthreads();
+  each([&](uint32_t key, int64_t i) {
+    if (key > lo || (key == lo && i <= a)) beam_push(sh, key, i);
+  });
+  __syncthreads();
+}
+
+// The k best continuations of a sentence, from its rows' sums and lists.
+__device__ __forceinline__ void beam_finish(const BeamArgs& p, BeamShared& sh, int64_t local) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int64_t b = p.first + local;
+  const float ninf = __int_as_float(0xff800000);
+  const uint2* sums = p.sums + local * p.beams * p.pieces;
+  const uint64_t* lists = p.lists + local * p.beams * p.pieces * p.k;
+  for (int i = warp; i < p.beams; i += kBeamThreads / 32) {
+    uint32_t top = 0;
+    for (int j = lane; j < p.pieces; j += 32) top = max(top, __ldcg(&sums[i * p.pieces + j].x));
+    top = __reduce_max_sync(0xffffffffu, top);
+    const bool bad = top >= 0xff800000u;  // +inf or NaN
+    const double m = top ? static_cast<double>(key_value(top)) : 0.0;
+    double sum = 0.0;
+    if (top && !bad)
+      for (int j = lane; j < p.pieces; j += 32) {
+        const uint2 s = __ldcg(&sums[i * p.pieces + j]);
+        if (s.x) sum += static_cast<double>(__uint_as_float(s.y)) * exp(static_cast<double>(key_value(s.x)) - m);
+      }
+#pragma unroll
+    for (int x = 16; x; x >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
+    if (lane == 0)
+      sh.off[i] = bad ? __longlong_as_double(0x7ff8000000000000ll)
+                      : static_cast<double>(__ldg(p.scores + b * p.beams + i)) - (m + log(sum));
+  }
+  if (tid == 0) sh.count = 0;
+  __syncthreads();
+  // Bound and gather as for a piece, on the values rounded down to float (the
+  // order is kept, equal ones stay candidates).
+  const int total = p.beams * p.pieces * p.k;
+  auto value = [&](int c, uint64_t e) {
+    return sh.off[c / (p.k * p.pieces)] + static_cast<double>(key_value(packed_key(e)));
+  };
+  auto low_key = [&](double v) { return order_key(__double2float_rd(v)); };
+  uint32_t mine = 0;
+  for (int c = tid; c < total; c += kBeamThreads) {
+    const uint64_t e = __ldcg(lists + c);
+    if (e) mine = max(mine, low_key(value(c, e)));
+  }
+  const uint32_t bound = max(beam_bound(mine, p.k, sh.warp_keys), 1u);
+  for (int c = tid; c < total; c += kBeamThreads) {
+    const uint64_t e = __ldcg(lists + c);
+    if (!e) continue;
+    const double v = value(c, e);
+    if (low_key(v) < bound) continue;
+    const int at = atomicAdd(&sh.count, 1);
+    if (at >= kBeamCap) continue;
+    sh.cont.value[at] = order_key64(v);
+    sh.cont.rest[at] = (static_cast<uint64_t>(~static_cast<uint32_t>(c / (p.k * p.pieces))) << 32) | packed_key(e);
+    sh.cont.token[at] = packed_idx(e);
+  }
+  __syncthreads();
+  const int m = sh.count;
+  auto write = [&](int64_t o, const Cont& c) {
+    const int i = static_cast<int>(~static_cast<uint32_t>(c.rest >> 32));
+    p.out_scores[o] = static_cast<float>(sh.off[i] + static_cast<double>(key_value(static_cast<uint32_t>(c.rest))));
+    p.out_parent[o] = i;
+    p.out_token[o] = static_cast<int32_t>(c.token);
+  };
+  int done = min(m, p.k);
+  if (m <= kBeamCap) {
+    for (int i = tid; i < m; i += kBeamThreads) {
+      const Cont mine = {sh.cont.value[i], sh.cont.rest[i], sh.cont.token[i]};
+      int above = 0;
+      for (int j = 0; j < m; ++j)
+        above += ranks_above(Cont{sh.cont.value[j], sh.cont.rest[j], sh.cont.token[j]}, mine);
+      if (above < p.k) write(b * p.k + above, mine);
+    }
+  } else {
+    // Too many near-equal values: one round over the lists per continuation.
+    Cont last = {~0ull, ~0ull, 0};
+    for (done = 0; done < p.k; ++done) {
+      Cont top = {0, 0, 0};
+      for (int c = tid; c < total; c += kBeamThreads) {
+        const uint64_t e = __ldcg(lists + c);
+        if (!e) continue;
+        const Cont x = {order_key64(value(c, e)),
+                        (static_cast<uint64_t>(~static_cast<uint32_t>(c / (p.k * p.pieces))) << 32) | packed_key(e),
+                        packed_idx(e)};
+        if ((done == 0 || ranks_above(last, x)) && ranks_above(x, top)) top = x;
+      }
+#pragma unroll
+      for (int x = 16; x; x >>= 1) {
+        const Cont y = {__shfl_xor_sync(0xffffffffu, top.value, x), __shfl_xor_sync(0xffffffffu, top.rest, x),
+                        __shfl_xor_sync(0xffffffffu, top.token, x)};
+        if (ranks_above(y, top)) top = y;
+      }
+      if (lane == 0) sh.best[warp] = top;
       __syncthreads();
+      last = sh.best[0];
+      for (int w = 1; w < kBeamThreads / 32; ++w)
+        if (ranks_above(sh.best[w], last)) last = sh.best[w];
+      __syncthreads();
+      if (last.value == 0) break;
+      if (tid == 0) write(b * p.k + done, last);
     }
-    last = best[0];
-    first = false;
-    const bool none = last.value == 0;
-    if (tid == 0) {
-      const int i = static_cast<int>(~static_cast<uint32_t>(last.rest >> 32));
-      const int64_t o = b * p.k + j;
-      p.out_scores[o] = none ? ninf : static_cast<float>(off[i] + static_cast<double>(key_value(static_cast<uint32_t>(last.rest))));
-      p.out_parent[o] = none ? -1 : i;
-      p.out_token[o] = none ? -1 : static_cast<int32_t>(last.token);
-    }
-    __syncthreads();
-    if (none) {
-      for (int r = j + 1 + tid; r < p.k; r += kBeamThreads) {
-        p.out_scores[b * p.k + r] = ninf;
-        p.out_parent[b * p.k + r] = -1;
-        p.out_token[b * p.k + r] = -1;
-      }
-      break;
-    }
+  }
+  for (int r = done + tid; r < p.k; r += kBeamThreads) {
+    p.out_scores[b * p.k + r] = ninf;
+    p.out_parent[b * p.k + r] = -1;
+    p.out_token[b * p.k + r] = -1;
   }
 }
 
+// Grid: sentence-major, then beam, then piece.
+template <typename T>
+__global__ void __launch_bounds__(kBeamThreads, 2) topk_beam_kernel(BeamArgs p) {
+  constexpr int kPer = BeamPiece<T>::kPer;
+  __shared__ BeamShared sh;
+  pdl_wait_then_release();
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int64_t row = blockIdx.x / p.pieces;  // of the launch
+  const int piece = static_cast<int>(blockIdx.x - row * p.pieces);
+  const int64_t local = row / p.beams;
+  uint2* sum_out = p.sums + blockIdx.x;
+  uint64_t* list = p.lists + static_cast<int64_t>(blockIdx.x) * p.k;
+  const float ninf = __int_as_float(0xff800000);
+  if (tid == 0) sh.count = 0;
+  if (__ldg(p.scores + p.first * p.beams + row) == ninf) {
+    if (tid == 0) *sum_out = make_uint2(0, 0);
+    for (int i = tid; i < p.k; i += kBeamThreads) list[i] = 0;
+  } else {
+    const T* row_x = static_cast<const T*>(p.logits) + (p.first * p.beams + row) * p.n;
+    const BeamPiece<T> pc(row_x, p.n, piece, p.pieces);
+    uint4 x[kBeamVectors];
+#pragma unroll
+    for (int v = 0; v < kBeamVectors; ++v) x[v] = pc.load(v);
+#pragma unroll
+    for (int v = 0; v < kBeamVectors; ++v)
+      if (pc.ragged(v)) x[v] = pc.load_ragged(v);
+    // largest element of the thread (NaN counts as the largest), and the bound
+    float top = ninf;
+#pragma unroll
+    for (int v = 0; v < kBeamVectors; ++v)
+#pragma unroll
+      for (int e = 0; e < kPer; e += 2) top = fmax3_nan(top, pc.value(x[v], e), pc.value(x[v], e + 1));
+    const uint32_t mine = beam_key(top);
+    const uint32_t bound = max(beam_bound(mine, p.k, sh.warp_keys), 1u);
+    // the piece's maximum
+    const uint32_t warp_top = __reduce_max_sync(0xffffffffu, mine);
+    __syncthreads();
+    if (lane == 0) sh.warp_keys[warp] = warp_top;
+    __syncthreads();
+    uint32_t key_top = 0;
+#pragma unroll
+    for (int w = 0; w < kBeamThreads / 32; ++w) key_top = max(key_top, sh.warp_keys[w]);
+    const bool bad = key_top >= 0xff800000u;
+    float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    if (!bad && key_top) {
+      const float m = key_value(key_top), least = key_value(bound == 1u ? 0x00800000u : bound);
+      constexpr float kLog2e = 1.4426950408889634f;
+#pragma unroll
+      for (int v = 0; v < kBeamVectors; ++v) {
+        float high = ninf;
+#pragma unroll
+        for (int e = 0; e < kPer; ++e) {
+          const float a = pc.value(x[v], e);
+          float y;
+          asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"((a - m) * kLog2e));
+          sum[e & 3] += y;
+          high = fmaxf(high, a);
+        }
+        if (high >= least) {
+#pragma unroll
+          for (int e = 0; e < kPer; ++e) {
+            const float a = pc.value(x[v], e);
+            if (a >= least) beam_push(sh, order_key(a), pc.index(v) + e);
+          }
+        }
+      }
+    } else if (bad) {
+#pragma unroll 1
+      for (int v = 0; v < kBeamVectors; ++v) {
+        const uint4 y = pc.ragged(v) ? pc.load_ragged(v) : pc.load(v);
+#pragma unroll
+        for (int e = 0; e < kPer; ++e) {
+          const uint32_t key = beam_key(pc.value(y, e));
+          if (key >= bound) beam_push(sh, key, pc.index(v) + e);
+        }
+      }
+    }
+    float s = (sum[0] + sum[1]) + (sum[2] + sum[3]);
+#pragma unroll
+    for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    if (lane == 0) sh.part[warp] = s;
+    __syncthreads();
+    if (sh.count > kBeamCap) beam_bisect(&sh, row_x, p.n, piece, p.pieces, p.k);
+    const int m = sh.count;
+    for (int i = tid; i < m; i += kBeamThreads) {
+      const uint64_t e = sh.gathered[i];
+      int above = 0;
+      for (int j = 0; j < m; ++j) above += sh.gathered[j] > e;
+      if (above < p.k) list[above] = e;
+    }
+    for (int i = m + tid; i < p.k; i += kBeamThreads) list[i] = 0;
+    if (tid == 0) {
+      double t = 0.0;
+#pragma unroll
+      for (int w = 0; w < kBeamThreads / 32; ++w) t += sh.part[w];
+      *sum_out = make_uint2(key_top, __float_as_uint(static_cast<float>(t)));
+    }
+  }
+  __threadfence();
+  __syncthreads();
+  if (tid == 0) {
+    const uint32_t n = static_cast<uint32_t>(p.beams) * p.pieces - 1;
+    sh.last = atomicAdd(p.tickets + local, 1u) == n;
+    if (sh.last) p.tickets[local] = 0;
+  }
+  __syncthreads();
+  if (!sh.last) return;
+  __threadfence();
+  beam_finish(p, sh, local);
+}
+
 // ---------------------------------------------------------------- reordering
+// A copy of rows, bound by memory: every kept row is read and written once.
+// Rows may start at any byte.  The body of a row is written in 16-byte vectors
+// on 16-byte addresses; where the source lies s bytes off such addresses, each
+// vector is shifted together from the two aligned ones that hold it (both
+// inside the row; the second is the next lane's first and comes from L1).
+// The up to 31 bytes before the body and 47 behind it are copied singly.
 constexpr int kReorderStates = 64;  // tensors per launch
+constexpr int kReorderThreads = 256;
+constexpr int kReorderUnroll = 8;
+constexpr int64_t kReorderChunk = kReorderThreads * kReorderUnroll * 16;  // bytes of a long row per item
+constexpr int64_t kReorderShort = 4096;  // rows up to this long go to one warp each
 
 struct ReorderArgs {
   const unsigned char* src[kReorderStates];  // [batch][beams][row_bytes]
   unsigned char* dst[kReorderStates];        // [batch][k][row_bytes]
   int64_t row_bytes[kReorderStates];
-  const int32_t* parents;  // [batch][k]
-  int64_t batch;
-  int beams, k;
+  int64_t end[kReorderStates];  // items of the tensors up to and with this one
+  const int32_t* parents;       // [batch][k]
+  int64_t rows;                 // batch * k
+  int count, beams, k;
 };
 
-// One CTA per (new beam, tensor).
-__global__ void __launch_bounds__(256) beam_reorder_simple(ReorderArgs p) {
-  pdl_wait_then_release();
-  const int s = blockIdx.y;
-  const int64_t r = blockIdx.x;
-  const int64_t nb = p.row_bytes[s];
-  const int32_t parent = __ldg(p.parents + r);
-  unsigned char* dst = p.dst[s] + r * nb;
-  if (parent < 0 || parent >= p.beams) {
-    if (parent != -1 && threadIdx.x == 0) atomicOr(&g_device_status, 2);
-    for (int64_t i = threadIdx.x; i < nb; i += 256) dst[i] = 0;
-    return;
+// Items (one CTA each) of a tensor: eight short rows, or a chunk of a long one.
+__host__ __device__ inline int64_t reorder_items(int64_t rows, int64_t row_bytes) {
+  if (row_bytes <= kReorderShort) return (rows + kReorderThreads / 32 - 1) / (kReorderThreads / 32);
+  return rows * ((row_bytes + kReorderChunk - 1) / kReorderChunk);
+}
+
+// 16 bytes from byte s (1 .. 15) on of two neighbouring vectors.
+__device__ __forceinline__ uint4 shift_together(const uint4& a, const uint4& b, int s) {
+  const int w = s >> 2, bits = (s & 3) * 8;
+  const uint32_t x0 = w == 0 ? a.x : w == 1 ? a.y : w == 2 ? a.z : a.w;
+  const uint32_t x1 = w == 0 ? a.y : w == 1 ? a.z : w == 2 ? a.w : b.x;
+  const uint32_t x2 = w == 0 ? a.z : w == 1 ? a.w : w == 2 ? b.x : b.y;
+  const uint32_t x3 = w == 0 ? a.w : w == 1 ? b.x : w == 2 ? b.y : b.z;
+  const uint32_t x4 = w == 0 ? b.x : w == 1 ? b.y : w == 2 ? b.z : b.w;
+  return make_uint4(__funnelshift_r(x0, x1, bits), __funnelshift_r(x1, x2, bits), __funnelshift_r(x2, x3, bits),
+                    __funnelshift_r(x3, x4, bits));
+}
+
+// Vectors [v0, v1) of a row's body and, where `edges`, the bytes around the
+// body, by `width` threads of which this is `id`.  src null: zeros.
+__device__ __forceinline__ void copy_row(unsigned char* dst, const unsigned char* src, int64_t bytes, int64_t v0,
+                                         int64_t v1, bool edges, int id, int width) {
+  int64_t head = static_cast<int64_t>((16 - (reinterpret_cast<uintptr_t>(dst) & 15)) & 15);
+  const int s = src ? static_cast<int>((reinterpret_cast<uintptr_t>(src) + head) & 15) : 0;
+  if (s > head) head += 16;
+  int64_t body = s ? (bytes - head + s) / 16 - 1 : (bytes - head) / 16;  // vectors whose sources lie in the row
+  if (bytes < head || body < 0) body = 0;
+  v1 = v1 < body ? v1 : body;
+  uint4* d = reinterpret_cast<uint4*>(dst + head);
+  const uint4* a = reinterpret_cast<const uint4*>(src + head - s);
+  for (int64_t i = v0 + id; i < v1; i += static_cast<int64_t>(width) * kReorderUnroll) {
+    uint4 x[kReorderUnroll];
+#pragma unroll
+    for (int u = 0; u < kReorderUnroll; ++u) {
+      const int64_t j = i + static_cast<int64_t>(u) * width;
+      x[u] = make_uint4(0, 0, 0, 0);
+      if (src && j < v1) x[u] = __ldg(a + j);
+    }
+    if (s) {
+#pragma unroll
+      for (int u = 0; u < kReorderUnroll; ++u) {
+        const int64_t j = i + static_cast<int64_t>(u) * width;
+        if (j < v1) x[u] = shift_together(x[u], __ldg(a + j + 1), s);
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < kReorderUnroll; ++u) {
+      const int64_t j = i + static_cast<int64_t>(u) * width;
+      if (j < v1) __stcs(d + j, x[u]);
+    }
   }
-  const unsigned char* src = p.src[s] + (r / p.k * p.beams + parent) * nb;
-  for (int64_t i = threadIdx.x; i < nb; i += 256) dst[i] = src[i];
+  if (edges) {
+    const int64_t behind = body ? head + body * 16 : 0;  // without a body: the whole row
+    const int64_t before = body ? head : 0;
+    for (int64_t i = id; i < before; i += width) dst[i] = src ? src[i] : 0;
+    for (int64_t i = behind + id; i < bytes; i += width) dst[i] = src ? src[i] : 0;
+  }
+}
+
+__global__ void __launch_bounds__(kReorderThreads) beam_reorder_kernel(ReorderArgs p) {
+  pdl_wait_then_release();
+  for (int64_t item = blockIdx.x; item < p.end[p.count - 1]; item += gridDim.x) {
+    int t = 0;
+    while (item >= p.end[t]) ++t;
+    int64_t i = item - (t ? p.end[t - 1] : 0);
+    const int64_t bytes = p.row_bytes[t];
+    int64_t r, chunk = 0;
+    int id = threadIdx.x, width = kReorderThreads;
+    if (bytes <= kReorderShort) {
+      r = i * (kReorderThreads / 32) + threadIdx.x / 32;
+      id = threadIdx.x & 31;
+      width = 32;
+      if (r >= p.rows) continue;
+    } else {
+      const int64_t chunks = (bytes + kReorderChunk - 1) / kReorderChunk;
+      r = i / chunks;
+      chunk = i - r * chunks;
+    }
+    const int32_t parent = __ldg(p.parents + r);
+    const bool live = parent >= 0 && parent < p.beams;
+    if (!live && parent != -1) atomicOr(&g_device_status, 2);
+    const unsigned char* src = live ? p.src[t] + (r / p.k * p.beams + parent) * bytes : nullptr;
+    copy_row(p.dst[t] + r * bytes, src, bytes, chunk * (kReorderChunk / 16), (chunk + 1) * (kReorderChunk / 16),
+             chunk == 0, id, width);
+  }
 }
 
 }  // namespace tk

@@ -19,6 +19,10 @@ namespace tk {
 
 namespace {
 
+// The part of a workspace that is zero between calls, of every operator.
+constexpr size_t kTicketBytes = 16384;
+static_assert(kTicketBytes >= 4 * kAttendMaxCtas && kTicketBytes >= 4 * kBeamTickets, "tickets");
+
 constexpr int kMaxReorder = 256;
 constexpr int64_t kMaxGridX = 2147483647LL;
 
@@ -80,7 +84,7 @@ constexpr int kAttendCtasPerSm = 2;
 
 size_t attend_workspace(int d, const DeviceInfo& dev) {
   const int ctas = std::min(dev.sms * kAttendCtasPerSm, kAttendMaxCtas);
-  return kAttendTicketBytes + static_cast<size_t>(ctas) * 2 * attend_part_floats(d) * 4;
+  return kTicketBytes + static_cast<size_t>(ctas) * 2 * attend_part_floats(d) * 4;
 }
 
 template <int D, bool kE4m3, bool kFull>
@@ -111,7 +115,7 @@ int launch_write(const WriteArgs& a, const DeviceInfo& dev, cudaStream_t st) {
   int rc = prepare_kernel(cache_write_kernel<D, kE4m3>);
   if (rc) return rc;
   const int64_t rows = a.tokens * a.cache[0].kv_heads * 2;
-  const int64_t per = 256 / (D / 8);
+  const int64_t per = 256 / (D / 16);
   const int64_t grid = std::min((rows + per - 1) / per, static_cast<int64_t>(dev.sms) * 8);
   return launch_pdl(cache_write_kernel<D, kE4m3>, dim3(static_cast<unsigned>(grid)), dim3(256), 0, st, a);
 }
@@ -120,9 +124,9 @@ template <int D, bool kE4m3>
 int launch_read(const ReadArgs& a, const DeviceInfo& dev, cudaStream_t st) {
   int rc = prepare_kernel(cache_read_kernel<D, kE4m3>);
   if (rc) return rc;
-  const int64_t rows = static_cast<int64_t>(a.tab.batch) * a.cache.kv_heads * a.n;
-  const int64_t per = 256 / (D / 8);
-  const int64_t grid = std::min((rows + per - 1) / per, static_cast<int64_t>(dev.sms) * 8);
+  (void)dev;
+  const int64_t blocks = (a.n + read_rows_per_cta<D>() - 1) / read_rows_per_cta<D>();
+  const int64_t grid = std::min(blocks * a.tab.batch * a.cache.kv_heads, kMaxGridX);
   return launch_pdl(cache_read_kernel<D, kE4m3>, dim3(static_cast<unsigned>(grid)), dim3(256), 0, st, a);
 }
 
@@ -132,20 +136,61 @@ int launch_read(const ReadArgs& a, const DeviceInfo& dev, cudaStream_t st) {
    : (d) == 128 ? ((e4m3) ? fn<128, true>(__VA_ARGS__) : fn<128, false>(__VA_ARGS__)) \
                 : ((e4m3) ? fn<256, true>(__VA_ARGS__) : fn<256, false>(__VA_ARGS__)))
 
+// Pieces of a beam's row: what the registers of a CTA hold at most, and down
+// to a quarter of that while the pieces are fewer than two per SM.
+int beam_pieces(int64_t rows, int64_t n, int esz, const DeviceInfo& dev) {
+  const int64_t vectors = n / (16 / esz) + 2;
+  const int64_t most = static_cast<int64_t>(kBeamThreads) * kBeamVectors;
+  const int64_t least = (vectors + most - 1) / most;
+  const int64_t wanted = std::min(2 * dev.sms / std::max<int64_t>(rows, 1), 4 * vectors / most);
+  return static_cast<int>(std::max(least, wanted));
+}
+
+struct BeamPlan {
+  int pieces;
+  int64_t sentences;  // per launch
+  size_t sums, lists; // bytes
+  size_t total() const { return kTicketBytes + sums + lists; }
+};
+
+BeamPlan plan_beam(int64_t batch, int beams, int64_t n, int k, int esz, const DeviceInfo& dev) {
+  BeamPlan pl;
+  pl.pieces = beam_pieces(batch * beams, n, esz, dev);
+  // as many sentences as have tickets and fit a grid and about 1 GB of lists
+  const int64_t row_bytes = static_cast<int64_t>(pl.pieces) * (8 + 8 * k) * beams;
+  const int64_t fit = std::min<int64_t>((int64_t{1} << 30) / row_bytes, kMaxGridX / (static_cast<int64_t>(pl.pieces) * beams));
+  pl.sentences = std::min(std::min(batch, static_cast<int64_t>(kBeamTickets)), std::max<int64_t>(fit, 1));
+  pl.sums = align_up(static_cast<size_t>(pl.sentences) * beams * pl.pieces * 8, 16);
+  pl.lists = static_cast<size_t>(pl.sentences) * beams * pl.pieces * k * 8;
+  return pl;
+}
+
 template <typename T>
 int run_beam(const T* logits, const float* scores, int64_t batch, int beams, int64_t n, int k, float* out_scores,
              int32_t* out_parent, int32_t* out_token, void* ws, size_t ws_bytes, void* stream) {
-  (void)ws;
-  (void)ws_bytes;
   if (!logits || !scores || !out_scores || !out_parent || !out_token) return TOPK_EINVAL;
   if (batch < 1 || beams < 1 || n < 1 || k < 1 || n > kMaxN) return TOPK_EINVAL;
   if (beams > TOPK_BEAM_MAX || k > TOPK_BEAM_MAX) return TOPK_EUNSUPPORTED;
   if (batch > kMaxElems / beams / n || batch > kMaxGridX) return TOPK_EUNSUPPORTED;
-  int rc = prepare_kernel(topk_beam_simple<T>);
+  if (reinterpret_cast<uintptr_t>(logits) % sizeof(T)) return TOPK_EINVAL;
+  DeviceInfo dev;
+  int rc = current_device_info(&dev);
   if (rc) return rc;
-  const BeamArgs a{logits, scores, n, beams, k, out_scores, out_parent, out_token};
-  return launch_pdl(topk_beam_simple<T>, dim3(static_cast<unsigned>(batch)), dim3(kBeamThreads), 0,
+  const BeamPlan pl = plan_beam(batch, beams, n, k, sizeof(T), dev);
+  if (!ws || ws_bytes < pl.total()) return TOPK_EWORKSPACE;
+  if (!aligned16(ws)) return TOPK_EINVAL;
+  BeamArgs a{logits, scores, n, beams, k, pl.pieces, 0, out_scores, out_parent, out_token, nullptr, nullptr, nullptr};
+  unsigned char* base = static_cast<unsigned char*>(ws);
+  a.tickets = reinterpret_cast<uint32_t*>(base);
+  a.sums = reinterpret_cast<uint2*>(base + kTicketBytes);
+  a.lists = reinterpret_cast<uint64_t*>(base + kTicketBytes + pl.sums);
+  for (; a.first < batch; a.first += pl.sentences) {
+    const int64_t rows = std::min(pl.sentences, batch - a.first) * beams;
+    rc = launch_pdl(topk_beam_kernel<T>, dim3(static_cast<unsigned>(rows * pl.pieces)), dim3(kBeamThreads), 0,
                     static_cast<cudaStream_t>(stream), a);
+    if (rc) return rc;
+  }
+  return TOPK_OK;
 }
 
 }  // namespace
@@ -190,7 +235,7 @@ int paged_attention(const uint16_t* q, int64_t q_stride, int64_t batch, int head
   if (!workspace || workspace_bytes < attend_workspace(k_cache->d, dev)) return TOPK_EWORKSPACE;
   if (!aligned16(workspace)) return TOPK_EINVAL;
   a.tickets = static_cast<uint32_t*>(workspace);
-  a.parts = reinterpret_cast<float*>(static_cast<unsigned char*>(workspace) + kAttendTicketBytes);
+  a.parts = reinterpret_cast<float*>(static_cast<unsigned char*>(workspace) + kTicketBytes);
   a.same_strides = a.k.page_stride == a.v.page_stride && a.k.head_stride == a.v.head_stride &&
                    a.k.token_stride == a.v.token_stride;
   a.q = q;
@@ -249,11 +294,11 @@ int cache_read(const topk_cache* cache, const int32_t* block_table, int64_t tabl
 }
 
 size_t topk_beam_workspace_bytes(int64_t batch, int beams, int64_t n, int k) {
-  (void)batch;
-  (void)beams;
-  (void)n;
-  (void)k;
-  return 0;
+  if (batch < 1 || beams < 1 || n < 1 || k < 1 || n > kMaxN || beams > TOPK_BEAM_MAX || k > TOPK_BEAM_MAX) return 0;
+  if (batch > kMaxElems / beams / n || batch > kMaxGridX) return 0;
+  DeviceInfo dev;
+  if (current_device_info(&dev)) return 0;
+  return std::max(plan_beam(batch, beams, n, k, 4, dev).total(), plan_beam(batch, beams, n, k, 2, dev).total());
 }
 
 int topk_beam(const float* logits, const float* beam_scores, int64_t batch, int beams, int64_t n, int k,
@@ -295,21 +340,24 @@ int beam_reorder(const void* const* src, void* const* dst, const int64_t* row_by
     any_end = std::max(any_end, span[i].end);
     if (span[i].dst) dst_end = std::max(dst_end, span[i].end);
   }
-  int rc = prepare_kernel(beam_reorder_simple);
+  int rc = prepare_kernel(beam_reorder_kernel);
   if (rc) return rc;
   for (int first = 0; first < count; first += kReorderStates) {
     ReorderArgs a{};
-    const int m = std::min(kReorderStates, count - first);
-    for (int i = 0; i < m; ++i) {
+    a.count = std::min(kReorderStates, count - first);
+    a.rows = batch * k;
+    int64_t items = 0;
+    for (int i = 0; i < a.count; ++i) {
       a.src[i] = static_cast<const unsigned char*>(src[first + i]);
       a.dst[i] = static_cast<unsigned char*>(dst[first + i]);
       a.row_bytes[i] = row_bytes[first + i];
+      items += reorder_items(a.rows, a.row_bytes[i]);
+      a.end[i] = items;
     }
     a.parents = parents;
-    a.batch = batch;
     a.beams = beams;
     a.k = k;
-    rc = launch_pdl(beam_reorder_simple, dim3(static_cast<unsigned>(batch * k), static_cast<unsigned>(m)), dim3(256),
+    rc = launch_pdl(beam_reorder_kernel, dim3(static_cast<unsigned>(std::min(items, kMaxGridX))), dim3(kReorderThreads),
                     0, static_cast<cudaStream_t>(stream), a);
     if (rc) return rc;
   }

@@ -98,57 +98,98 @@ struct WriteArgs {
   int64_t tokens;
 };
 
-// One group of D / 8 lanes per row (16 bytes a lane).
+// D / 16 lanes per row, 16 values a lane; kWriteRows rows of a lane group in
+// flight.  Rows (token, k or v, head) are numbered in that order, so that
+// neighbouring groups read neighbouring memory; a group's next row is found by
+// addition (a 64-bit division per row costs more than the row's bytes).
+// Bound by memory: every value is read once (2 bytes) and written once.
+constexpr int kWriteRows = 4;
+
 template <int D, bool kE4m3>
 __global__ void __launch_bounds__(256) cache_write_kernel(WriteArgs p) {
-  constexpr int L = D / 8;
+  constexpr int L = D / 16;
   pdl_wait_then_release();
   const int heads = p.cache[0].kv_heads;
-  const int64_t rows = p.tokens * heads * 2;
+  const int lines = 2 * heads;  // rows of a token
+  const int64_t rows = p.tokens * lines;
   const int64_t groups = static_cast<int64_t>(gridDim.x) * (256 / L);
+  const int64_t token_step = groups / lines;
+  const int line_step = static_cast<int>(groups - token_step * lines);
   const int gl = threadIdx.x % L;
-  const unsigned mask = L == 32 ? 0xffffffffu : ((1u << L) - 1u) << (threadIdx.x % 32 / L * L);
-  for (int64_t r = static_cast<int64_t>(blockIdx.x) * (256 / L) + threadIdx.x / L; r < rows; r += groups) {
-    const int w = static_cast<int>(r & 1);
-    const int h = static_cast<int>((r >> 1) % heads);
-    const int64_t t = (r >> 1) / heads;
-    const int64_t slot = __ldg(p.slots + t);
-    if (slot < 0) continue;
-    const CacheView& c = p.cache[w];
-    const int64_t page = slot / c.page_size;
-    if (page >= c.pages) {
-      atomicOr(&g_device_status, kDevBadIndex);
-      continue;
-    }
-    const int off = static_cast<int>(slot - page * c.page_size);
-    const uint4 x = *reinterpret_cast<const uint4*>(p.src[w] + t * p.token_stride[w] + h * p.head_stride[w] + gl * 8);
-    unsigned char* dst = c.data + page * c.page_stride + h * c.head_stride + off * c.token_stride;
-    if constexpr (!kE4m3) {
-      *reinterpret_cast<uint4*>(dst + gl * 16) = x;
-    } else {
-      const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
-      float f[8];
-      uint32_t top = 0;
+  const unsigned mask = ((1u << L) - 1u) << (threadIdx.x % 32 / L * L);
+  int64_t r = static_cast<int64_t>(blockIdx.x) * (256 / L) + threadIdx.x / L;
+  int64_t t = r / lines;
+  int line = static_cast<int>(r - t * lines);
+  while (r < rows) {
+    int64_t slot[kWriteRows];
+    int64_t tok[kWriteRows];
+    int ln[kWriteRows];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        f[2 * i] = __uint_as_float(xs[i] << 16);
-        f[2 * i + 1] = __uint_as_float(xs[i] & 0xffff0000u);
-        top = max(top, max((xs[i] << 16) & 0x7fff0000u, xs[i] & 0x7fff0000u));
+    for (int i = 0; i < kWriteRows; ++i) {
+      tok[i] = t;
+      ln[i] = line;
+      slot[i] = r < rows ? __ldg(p.slots + t) : -1;
+      r += groups;
+      t += token_step;
+      line += line_step;
+      if (line >= lines) {
+        line -= lines;
+        ++t;
       }
+    }
+    uint4 x[kWriteRows][2];
 #pragma unroll
-      for (int o = L / 2; o >= 1; o >>= 1) top = max(top, __shfl_xor_sync(mask, top, o));
-      const bool finite = top < 0x7f800000u;
-      const int e = row_exponent(top);
-      const float inv = finite ? power_of_two(-e) : __uint_as_float(0x7fffffffu);
-      uint32_t out[2];
+    for (int i = 0; i < kWriteRows; ++i) {
+      const int w = ln[i] >= heads ? 1 : 0, h = ln[i] - w * heads;
+      const uint4* src = reinterpret_cast<const uint4*>((w ? p.src[1] : p.src[0]) +
+                                                        tok[i] * (w ? p.token_stride[1] : p.token_stride[0]) +
+                                                        h * (w ? p.head_stride[1] : p.head_stride[0])) +
+                         gl * 2;
+      x[i][0] = x[i][1] = make_uint4(0, 0, 0, 0);
+      if (slot[i] >= 0) {
+        x[i][0] = __ldcs(src);
+        x[i][1] = __ldcs(src + 1);
+      }
+    }
 #pragma unroll
-      for (int i = 0; i < 2; ++i)
-        out[i] = floats_to_e4m3x2(f[4 * i] * inv, f[4 * i + 1] * inv) |
-                 (floats_to_e4m3x2(f[4 * i + 2] * inv, f[4 * i + 3] * inv) << 16);
-      *reinterpret_cast<uint2*>(dst + gl * 8) = make_uint2(out[0], out[1]);
-      if (gl == 0)
-        c.scale[page * c.s_page_stride + h * c.s_head_stride + off * c.s_token_stride] =
-            finite ? power_of_two(e) : __uint_as_float(0x7fffffffu);
+    for (int i = 0; i < kWriteRows; ++i) {
+      if (slot[i] < 0) continue;  // the same for a group's lanes
+      const int w = ln[i] >= heads ? 1 : 0, h = ln[i] - w * heads;
+      const CacheView& c = p.cache[w];
+      const int64_t page = (slot[i] >> 32) == 0
+                               ? static_cast<int64_t>(static_cast<uint32_t>(slot[i]) / static_cast<uint32_t>(c.page_size))
+                               : slot[i] / c.page_size;
+      if (page >= c.pages) {
+        atomicOr(&g_device_status, kDevBadIndex);
+        continue;
+      }
+      const int off = static_cast<int>(slot[i] - page * c.page_size);
+      unsigned char* dst = c.data + page * c.page_stride + h * c.head_stride + off * c.token_stride;
+      if constexpr (!kE4m3) {
+        reinterpret_cast<uint4*>(dst)[gl * 2] = x[i][0];
+        reinterpret_cast<uint4*>(dst)[gl * 2 + 1] = x[i][1];
+      } else {
+        const uint32_t xs[8] = {x[i][0].x, x[i][0].y, x[i][0].z, x[i][0].w, x[i][1].x, x[i][1].y, x[i][1].z, x[i][1].w};
+        uint32_t top = 0;
+#pragma unroll
+        for (int y = 0; y < 8; ++y) top = max(top, max((xs[y] << 16) & 0x7fff0000u, xs[y] & 0x7fff0000u));
+#pragma unroll
+        for (int o = L / 2; o >= 1; o >>= 1) top = max(top, __shfl_xor_sync(mask, top, o));
+        const bool finite = top < 0x7f800000u;
+        const int e = row_exponent(top);
+        const float inv = finite ? power_of_two(-e) : __uint_as_float(0x7fffffffu);
+        uint32_t out[4];
+#pragma unroll
+        for (int y = 0; y < 4; ++y)
+          out[y] = floats_to_e4m3x2(__uint_as_float(xs[2 * y] << 16) * inv, __uint_as_float(xs[2 * y] & 0xffff0000u) * inv) |
+                   (floats_to_e4m3x2(__uint_as_float(xs[2 * y + 1] << 16) * inv,
+                                     __uint_as_float(xs[2 * y + 1] & 0xffff0000u) * inv)
+                    << 16);
+        reinterpret_cast<uint4*>(dst)[gl] = make_uint4(out[0], out[1], out[2], out[3]);
+        if (gl == 0)
+          c.scale[page * c.s_page_stride + h * c.s_head_stride + off * c.s_token_stride] =
+              finite ? power_of_two(e) : __uint_as_float(0x7fffffffu);
+      }
     }
   }
 }
@@ -161,46 +202,85 @@ struct ReadArgs {
   uint16_t* out;  // [batch][kv_heads][n][d] bf16
 };
 
-// One group of D / 8 lanes per row of the output; rows past a sequence's end
-// (and rows whose page does not exist) are zero.
+// A CTA reads 256 / (D / 16) * kReadRows successive rows of one sequence and
+// head: D / 16 lanes per row, 16 values a lane, kReadRows rows of a lane group
+// in flight.  Rows past a sequence's end (and rows whose page does not exist)
+// are zero.  Bound by memory: the cached row read once, 2 bytes a value written.
+constexpr int kReadRows = 4;
+
+template <int D>
+__host__ __device__ constexpr int read_rows_per_cta() {
+  return 256 / (D / 16) * kReadRows;
+}
+
 template <int D, bool kE4m3>
 __global__ void __launch_bounds__(256) cache_read_kernel(ReadArgs p) {
-  constexpr int L = D / 8;
+  constexpr int L = D / 16, kGroups = 256 / L;
   pdl_wait_then_release();
   const CacheView& c = p.cache;
-  const int64_t rows = static_cast<int64_t>(p.tab.batch) * c.kv_heads * p.n;
-  const int64_t groups = static_cast<int64_t>(gridDim.x) * (256 / L);
-  const int gl = threadIdx.x % L;
-  for (int64_t r = static_cast<int64_t>(blockIdx.x) * (256 / L) + threadIdx.x / L; r < rows; r += groups) {
-    const int64_t bh = r / p.n;
-    const int64_t t = r - bh * p.n;
+  const int64_t blocks = (p.n + read_rows_per_cta<D>() - 1) / read_rows_per_cta<D>();  // of a sequence and head
+  const int64_t items = blocks * p.tab.batch * c.kv_heads;
+  const int gl = threadIdx.x % L, g = threadIdx.x / L;
+  for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
+    const int64_t bh = item / blocks;
     const int b = static_cast<int>(bh / c.kv_heads), h = static_cast<int>(bh - static_cast<int64_t>(b) * c.kv_heads);
-    uint4 x = make_uint4(0, 0, 0, 0);
-    if (t < seq_length(p.tab, b)) {
-      const int64_t at = t / c.page_size;
-      const int off = static_cast<int>(t - at * c.page_size);
-      const int32_t page = __ldg(p.tab.table + b * p.tab.stride + at);
-      if (page < 0 || page >= c.pages) {
-        atomicOr(&g_device_status, kDevBadIndex);
-      } else {
-        const unsigned char* src = c.data + page * c.page_stride + h * c.head_stride + off * c.token_stride;
-        if constexpr (!kE4m3) {
-          x = __ldg(reinterpret_cast<const uint4*>(src + gl * 16));
-        } else {
-          const uint2 w = __ldg(reinterpret_cast<const uint2*>(src + gl * 8));
-          const float s = __ldg(c.scale + page * c.s_page_stride + h * c.s_head_stride + off * c.s_token_stride);
-          const uint32_t two[4] = {w.x & 0xffffu, w.x >> 16, w.y & 0xffffu, w.y >> 16};
-          uint32_t o[4];
+    const int64_t t0 = (item - bh * blocks) * read_rows_per_cta<D>() + g;
+    const int len = seq_length(p.tab, b);
+    int32_t page[kReadRows];
+    int off[kReadRows];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float2 f = f16x2_to_float2(e4m3x2_to_f16x2(two[i]));
-            o[i] = floats_to_bf16x2(f.x * s, f.y * s);
-          }
-          x = make_uint4(o[0], o[1], o[2], o[3]);
+    for (int i = 0; i < kReadRows; ++i) {
+      const int64_t t = t0 + i * kGroups;
+      page[i] = -1;
+      off[i] = 0;
+      if (t < len && t < p.n) {
+        const int at = static_cast<int>(t) / c.page_size;
+        off[i] = static_cast<int>(t) - at * c.page_size;
+        page[i] = __ldg(p.tab.table + b * p.tab.stride + at);
+        if (page[i] < 0 || page[i] >= c.pages) {
+          atomicOr(&g_device_status, kDevBadIndex);
+          page[i] = -1;
         }
       }
     }
-    *reinterpret_cast<uint4*>(p.out + r * D + gl * 8) = x;
+    uint4 x[kReadRows][2];
+    float s[kReadRows];
+#pragma unroll
+    for (int i = 0; i < kReadRows; ++i) {
+      x[i][0] = x[i][1] = make_uint4(0, 0, 0, 0);
+      s[i] = 0.0f;
+      if (page[i] >= 0) {
+        const uint4* src = reinterpret_cast<const uint4*>(c.data + page[i] * c.page_stride + h * c.head_stride +
+                                                          off[i] * c.token_stride);
+        if constexpr (kE4m3) {
+          x[i][0] = __ldg(src + gl);
+          s[i] = __ldg(c.scale + page[i] * c.s_page_stride + h * c.s_head_stride + off[i] * c.s_token_stride);
+        } else {
+          x[i][0] = __ldg(src + gl * 2);
+          x[i][1] = __ldg(src + gl * 2 + 1);
+        }
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kReadRows; ++i) {
+      const int64_t t = t0 + i * kGroups;
+      if (t >= p.n) continue;
+      uint4 o0 = x[i][0], o1 = x[i][1];
+      if constexpr (kE4m3) {
+        const uint32_t w[4] = {x[i][0].x, x[i][0].y, x[i][0].z, x[i][0].w};
+        uint32_t o[8];
+#pragma unroll
+        for (int y = 0; y < 8; ++y) {
+          const float2 f = f16x2_to_float2(e4m3x2_to_f16x2(y & 1 ? w[y / 2] >> 16 : w[y / 2] & 0xffffu));
+          o[y] = floats_to_bf16x2(f.x * s[i], f.y * s[i]);
+        }
+        o0 = make_uint4(o[0], o[1], o[2], o[3]);
+        o1 = make_uint4(o[4], o[5], o[6], o[7]);
+      }
+      uint4* dst = reinterpret_cast<uint4*>(p.out + (bh * p.n + t) * D) + gl * 2;
+      __stcs(dst, o0);
+      __stcs(dst + 1, o1);
+    }
   }
 }
 

@@ -47,7 +47,6 @@ struct AttendArgs {
 constexpr int kAttendWarps = 4;
 constexpr int kAttendThreads = 32 * kAttendWarps;
 constexpr int kAttendMaxCtas = 1024;
-constexpr size_t kAttendTicketBytes = kAttendMaxCtas * 4;
 
 __host__ __device__ constexpr int attend_part_floats(int d) { return 16 * (d + 2); }
 
