@@ -56,6 +56,12 @@ __device__ __forceinline__ bool ranks_above(const Cont& a, const Cont& b) {
 // Bound by reading the logits.  A logit costs one exponential (16 per clock
 // and SM: 4.5e12 a second, against 1.6e12 fp32 or 3.2e12 bf16 logits a second
 // at full bandwidth) and about six other instructions.
+// A piece's largest key (0: nothing) and sum of exp(x - max).
+struct __align__(16) BeamSum {
+  double sum;
+  uint32_t top;
+};
+
 struct BeamArgs {
   const void* logits;   // [batch][beams][n]
   const float* scores;  // [batch][beams]
@@ -67,13 +73,17 @@ struct BeamArgs {
   int32_t* out_parent;  // [batch][k]
   int32_t* out_token;   // [batch][k]
   uint32_t* tickets;    // [sentences of the launch], zero between calls
-  uint2* sums;          // [rows of the launch][pieces]: key of the maximum, sum of 2^((x - max) log2 e)
+  BeamSum* sums;        // [rows of the launch][pieces]
   uint64_t* lists;      // [rows of the launch][pieces][k]
 };
 
 constexpr int kMaxBeams = 128;
 constexpr int kBeamCap = 512;       // gathered candidates; more than the largest k
-constexpr int kBeamVectors = 16;    // 16-byte vectors per thread
+#ifndef BV
+#define BV 16
+#define BC 2
+#endif
+constexpr int kBeamVectors = BV;    // 16-byte vectors per thread
 constexpr int kBeamTickets = 4096;  // sentences per launch
 
 // Order key of a candidate logit; 0 for one that gives no continuation.
@@ -132,6 +142,12 @@ struct BeamShared {
   int count, total, last;
 };
 
+__device__ __forceinline__ float exp2_ftz(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
 // The piece of a row that a CTA takes, as 16-byte vectors on 16-byte addresses:
 // vector v of a thread holds the row's elements from index(v) on.  A vector
 // behind the piece, and elements outside the row, read as -inf.
@@ -143,29 +159,39 @@ struct BeamPiece {
   int64_t n;
   int64_t w0, w1;  // vectors of the piece
   int mis;         // elements of the row's first vector that lie before the row
+  int low, count;  // vectors of the piece from w0 + low on that lie inside the row: `count`
 
   __device__ __forceinline__ BeamPiece(const T* row_, int64_t n_, int piece, int pieces) : row(row_), n(n_) {
     mis = static_cast<int>((reinterpret_cast<uintptr_t>(row) / sizeof(T)) % kPer);
     const int64_t vectors = (n + mis + kPer - 1) / kPer;
     w0 = vectors * piece / pieces;
     w1 = vectors * (piece + 1) / pieces;
+    low = first_ragged() >= 0;
+    count = static_cast<int>(w1 - w0) - low - (last_ragged() >= 0);
   }
   __device__ __forceinline__ int64_t vector(int v) const { return w0 + v * kBeamThreads + threadIdx.x; }
   __device__ __forceinline__ int64_t index(int v) const { return vector(v) * kPer - mis; }
   __device__ __forceinline__ bool inside(int64_t w) const { return w * kPer >= mis && (w + 1) * kPer - mis <= n; }
+  // A vector inside the row; what is ragged reads as -inf.
   __device__ __forceinline__ uint4 load(int v) const {
-    const int64_t w = vector(v);
     uint4 x = make_uint4(kFill, kFill, kFill, kFill);
-    if (w < w1 && inside(w)) x = __ldcs(reinterpret_cast<const uint4*>(row - mis + w * kPer));
+    const int i = v * kBeamThreads + static_cast<int>(threadIdx.x);
+    if (static_cast<unsigned>(i - low) < static_cast<unsigned>(count))
+      x = __ldg(reinterpret_cast<const uint4*>(row - mis + w0 * kPer) + i);
     return x;
   }
-  // The row's first or last vector, which may hold elements of its neighbours.
-  __device__ __forceinline__ bool ragged(int v) const { return vector(v) < w1 && !inside(vector(v)); }
-  __device__ __forceinline__ uint4 load_ragged(int v) const {
+  // The row's first and last vector, if this piece holds them and they hold
+  // elements of the row's neighbours too; else -1.  (One that is both is first.)
+  __device__ __forceinline__ int64_t first_ragged() const { return w0 == 0 && w1 > 0 && !inside(0) ? 0 : -1; }
+  __device__ __forceinline__ int64_t last_ragged() const {
+    const int64_t w = (n + mis + kPer - 1) / kPer - 1;
+    return w1 > w && w0 <= w && w > 0 && !inside(w) ? w : -1;
+  }
+  __device__ __forceinline__ uint4 load_ragged(int64_t w) const {
     uint32_t word[4] = {kFill, kFill, kFill, kFill};
 #pragma unroll
     for (int e = 0; e < kPer; ++e) {
-      const int64_t i = index(v) + e;
+      const int64_t i = w * kPer - mis + e;
       if (i < 0 || i >= n) continue;
       if constexpr (sizeof(T) == 4)
         word[e] = __float_as_uint(row[i]);
@@ -174,6 +200,39 @@ struct BeamPiece {
                             : (word[e / 2] & 0xffff0000u) | row[i];
     }
     return make_uint4(word[0], word[1], word[2], word[3]);
+  }
+  // Elementwise larger (NaN is the largest), two bf16 at a time.
+  static __device__ __forceinline__ uint4 larger(const uint4& a, const uint4& b) {
+    return make_uint4(larger(a.x, b.x), larger(a.y, b.y), larger(a.z, b.z), larger(a.w, b.w));
+  }
+  static __device__ __forceinline__ uint32_t larger(uint32_t a, uint32_t b) {
+    if constexpr (sizeof(T) == 4) return __float_as_uint(fmax_nan(__uint_as_float(a), __uint_as_float(b)));
+    uint32_t d;
+    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+  }
+  static __device__ __forceinline__ float largest(const uint4& x) {
+    const uint32_t w = larger(larger(x.x, x.y), larger(x.z, x.w));
+    if constexpr (sizeof(T) == 4) return __uint_as_float(w);
+    return fmax_nan(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+  }
+  // A float's bits (exact in T) as the word reaches() compares with.
+  static __device__ __forceinline__ uint32_t bits(uint32_t f) {
+    return sizeof(T) == 4 ? f : (f & 0xffff0000u) | (f >> 16);
+  }
+  // Whether an element (none of them NaN) is at least `least`.
+  static __device__ __forceinline__ bool reaches(const uint4& x, uint32_t least) {
+    const uint32_t w = larger(larger(x.x, x.y), larger(x.z, x.w));
+    if constexpr (sizeof(T) == 4) return __uint_as_float(w) >= __uint_as_float(least);
+    uint32_t d;
+    asm("set.ge.u32.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(w), "r"(least));
+    return d != 0;
+  }
+  static __device__ __forceinline__ float value_at(const uint4& x, int e) {  // e not known when compiling
+    const int i = sizeof(T) == 4 ? e : e >> 1;
+    const uint32_t w = i == 0 ? x.x : i == 1 ? x.y : i == 2 ? x.z : x.w;
+    if constexpr (sizeof(T) == 4) return __uint_as_float(w);
+    return __uint_as_float(e & 1 ? w & 0xffff0000u : w << 16);
   }
   static __device__ __forceinline__ float value(const uint4& x, int e) {
     const int i = e * static_cast<int>(sizeof(T)) / 4;
@@ -198,7 +257,8 @@ __device__ __noinline__ void beam_bisect(BeamShared* shp, const T* row, int64_t 
   auto each = [&](auto&& f) {
 #pragma unroll 1
     for (int v = 0; v < kBeamVectors; ++v) {
-      const uint4 x = p.ragged(v) ? p.load_ragged(v) : p.load(v);
+      const int64_t w = p.vector(v);
+      const uint4 x = w < p.w1 && !p.inside(w) ? p.load_ragged(w) : p.load(v);
 #pragma unroll
       for (int e = 0; e < p.kPer; ++e) f(beam_key(p.value(x, e)), p.index(v) + e);
     }
@@ -240,19 +300,20 @@ __device__ __forceinline__ void beam_finish(const BeamArgs& p, BeamShared& sh, i
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int64_t b = p.first + local;
   const float ninf = __int_as_float(0xff800000);
-  const uint2* sums = p.sums + local * p.beams * p.pieces;
+  const BeamSum* sums = p.sums + local * p.beams * p.pieces;
   const uint64_t* lists = p.lists + local * p.beams * p.pieces * p.k;
   for (int i = warp; i < p.beams; i += kBeamThreads / 32) {
     uint32_t top = 0;
-    for (int j = lane; j < p.pieces; j += 32) top = max(top, __ldcg(&sums[i * p.pieces + j].x));
+    for (int j = lane; j < p.pieces; j += 32) top = max(top, __ldcg(&sums[i * p.pieces + j].top));
     top = __reduce_max_sync(0xffffffffu, top);
     const bool bad = top >= 0xff800000u;  // +inf or NaN
     const double m = top ? static_cast<double>(key_value(top)) : 0.0;
     double sum = 0.0;
     if (top && !bad)
       for (int j = lane; j < p.pieces; j += 32) {
-        const uint2 s = __ldcg(&sums[i * p.pieces + j]);
-        if (s.x) sum += static_cast<double>(__uint_as_float(s.y)) * exp(static_cast<double>(key_value(s.x)) - m);
+        const uint32_t t = __ldcg(&sums[i * p.pieces + j].top);
+        const double x = __ldcg(&sums[i * p.pieces + j].sum);
+        if (t) sum += x * exp(static_cast<double>(key_value(t)) - m);
       }
 #pragma unroll
     for (int x = 16; x; x >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
@@ -262,8 +323,8 @@ __device__ __forceinline__ void beam_finish(const BeamArgs& p, BeamShared& sh, i
   }
   if (tid == 0) sh.count = 0;
   __syncthreads();
-  // Bound and gather as for a piece, on the values rounded down to float (the
-  // order is kept, equal ones stay candidates).
+  // Bound and gather on the values rounded down to float (the order is kept,
+  // equal ones stay candidates).
   const int total = p.beams * p.pieces * p.k;
   auto value = [&](int c, uint64_t e) {
     return sh.off[c / (p.k * p.pieces)] + static_cast<double>(key_value(packed_key(e)));
@@ -274,7 +335,14 @@ __device__ __forceinline__ void beam_finish(const BeamArgs& p, BeamShared& sh, i
     const uint64_t e = __ldcg(lists + c);
     if (e) mine = max(mine, low_key(value(c, e)));
   }
-  const uint32_t bound = max(beam_bound(mine, p.k, sh.warp_keys), 1u);
+  // The k-th largest of the threads' maxima, to 20 bits: beams differ in score,
+  // so the bound of the weakest warp would let most candidates through.
+  uint32_t bound = 0;
+  for (int bit = 31; bit >= 12; --bit) {
+    const uint32_t trial = bound | (1u << bit);
+    if (__syncthreads_count(mine >= trial) >= p.k) bound = trial;
+  }
+  bound = max(bound, 1u);
   for (int c = tid; c < total; c += kBeamThreads) {
     const uint64_t e = __ldcg(lists + c);
     if (!e) continue;
@@ -341,7 +409,7 @@ __device__ __forceinline__ void beam_finish(const BeamArgs& p, BeamShared& sh, i
 
 // Grid: sentence-major, then beam, then piece.
 template <typename T>
-__global__ void __launch_bounds__(kBeamThreads, 2) topk_beam_kernel(BeamArgs p) {
+__global__ void __launch_bounds__(kBeamThreads, BC) topk_beam_kernel(BeamArgs p) {
   constexpr int kPer = BeamPiece<T>::kPer;
   __shared__ BeamShared sh;
   pdl_wait_then_release();
@@ -349,12 +417,12 @@ __global__ void __launch_bounds__(kBeamThreads, 2) topk_beam_kernel(BeamArgs p) 
   const int64_t row = blockIdx.x / p.pieces;  // of the launch
   const int piece = static_cast<int>(blockIdx.x - row * p.pieces);
   const int64_t local = row / p.beams;
-  uint2* sum_out = p.sums + blockIdx.x;
+  BeamSum* sum_out = p.sums + blockIdx.x;
   uint64_t* list = p.lists + static_cast<int64_t>(blockIdx.x) * p.k;
   const float ninf = __int_as_float(0xff800000);
   if (tid == 0) sh.count = 0;
   if (__ldg(p.scores + p.first * p.beams + row) == ninf) {
-    if (tid == 0) *sum_out = make_uint2(0, 0);
+    if (tid == 0) *sum_out = BeamSum{0.0, 0u};
     for (int i = tid; i < p.k; i += kBeamThreads) list[i] = 0;
   } else {
     const T* row_x = static_cast<const T*>(p.logits) + (p.first * p.beams + row) * p.n;
@@ -362,15 +430,18 @@ __global__ void __launch_bounds__(kBeamThreads, 2) topk_beam_kernel(BeamArgs p) 
     uint4 x[kBeamVectors];
 #pragma unroll
     for (int v = 0; v < kBeamVectors; ++v) x[v] = pc.load(v);
-#pragma unroll
-    for (int v = 0; v < kBeamVectors; ++v)
-      if (pc.ragged(v)) x[v] = pc.load_ragged(v);
+    // The row's ragged first and last vector go to threads 0 and 32.
+    uint4 edge = make_uint4(pc.kFill, pc.kFill, pc.kFill, pc.kFill);
+    const int64_t edge_at = tid == 0 ? pc.first_ragged() : tid == 32 ? pc.last_ragged() : -1;
+    if (edge_at >= 0) edge = pc.load_ragged(edge_at);
     // largest element of the thread (NaN counts as the largest), and the bound
-    float top = ninf;
+    float top = pc.largest(edge);
+    {
+      uint4 y = x[0];
 #pragma unroll
-    for (int v = 0; v < kBeamVectors; ++v)
-#pragma unroll
-      for (int e = 0; e < kPer; e += 2) top = fmax3_nan(top, pc.value(x[v], e), pc.value(x[v], e + 1));
+      for (int v = 1; v < kBeamVectors; ++v) y = pc.larger(y, x[v]);
+      top = fmax_nan(top, pc.largest(y));
+    }
     const uint32_t mine = beam_key(top);
     const uint32_t bound = max(beam_bound(mine, p.k, sh.warp_keys), 1u);
     // the piece's maximum
@@ -381,60 +452,78 @@ __global__ void __launch_bounds__(kBeamThreads, 2) topk_beam_kernel(BeamArgs p) 
     uint32_t key_top = 0;
 #pragma unroll
     for (int w = 0; w < kBeamThreads / 32; ++w) key_top = max(key_top, sh.warp_keys[w]);
-    const bool bad = key_top >= 0xff800000u;
+    // The sum of 2^(x L - M), M = m L rounded, L = log2 e rounded: one fused
+    // multiply-add and one exponential a logit.  M's rounding is taken out
+    // exactly at the end (M - m L is known in 64 bits); L's moves the exponent
+    // of a term by 2^-26 of (x - m) log2 e.
+    constexpr float kLog2e = 1.4426950408889634f;
     float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    if (!bad && key_top) {
-      const float m = key_value(key_top), least = key_value(bound == 1u ? 0x00800000u : bound);
-      constexpr float kLog2e = 1.4426950408889634f;
-#pragma unroll
-      for (int v = 0; v < kBeamVectors; ++v) {
-        float high = ninf;
-#pragma unroll
-        for (int e = 0; e < kPer; ++e) {
-          const float a = pc.value(x[v], e);
-          float y;
-          asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"((a - m) * kLog2e));
-          sum[e & 3] += y;
-          high = fmaxf(high, a);
-        }
-        if (high >= least) {
-#pragma unroll
-          for (int e = 0; e < kPer; ++e) {
-            const float a = pc.value(x[v], e);
-            if (a >= least) beam_push(sh, order_key(a), pc.index(v) + e);
-          }
-        }
-      }
-    } else if (bad) {
+    double fix = 0.0;   // log2 of what the sum is to be multiplied by
+    uint32_t hits = 0;  // vectors with an element at or above the bound
+    const float m = key_top ? key_value(key_top) : 0.0f;
+    const uint32_t least = pc.bits(bound == 1u ? 0xff7fffffu : __float_as_uint(key_value(bound)));
+    if (key_top >= 0xff800000u) {  // a NaN or +inf: no sum, and every vector is looked at
+      hits = (1u << kBeamVectors) - 1;
+    } else if (fabsf(m) > 1e6f) {  // m L would be off by more than a fraction of 1
+      hits = (1u << kBeamVectors) - 1;
 #pragma unroll 1
-      for (int v = 0; v < kBeamVectors; ++v) {
-        const uint4 y = pc.ragged(v) ? pc.load_ragged(v) : pc.load(v);
+      for (int v = 0; v <= kBeamVectors; ++v) {
+        const uint4 y = v < kBeamVectors ? pc.load(v) : edge;
 #pragma unroll
-        for (int e = 0; e < kPer; ++e) {
-          const uint32_t key = beam_key(pc.value(y, e));
-          if (key >= bound) beam_push(sh, key, pc.index(v) + e);
-        }
+        for (int e = 0; e < kPer; ++e) sum[e & 3] += exp2_ftz((pc.value(y, e) - m) * kLog2e);
       }
+    } else if (key_top) {
+      const float ml = m * kLog2e;
+      fix = static_cast<double>(ml) - static_cast<double>(m) * static_cast<double>(kLog2e);
+#pragma unroll
+      for (int v = 0; v < kBeamVectors; ++v) {
+#pragma unroll
+        for (int e = 0; e < kPer; ++e) sum[e & 3] += exp2_ftz(fmaf(pc.value(x[v], e), kLog2e, -ml));
+        hits |= pc.reaches(x[v], least) ? 1u << v : 0u;
+      }
+      if (edge_at >= 0)
+#pragma unroll
+        for (int e = 0; e < kPer; ++e) sum[e & 3] += exp2_ftz(fmaf(pc.value(edge, e), kLog2e, -ml));
     }
+    // The hits' elements are read once more (from L2), which keeps this loop small.
+    const float floor_value = bound == 1u ? ninf : key_value(bound);
+    auto gather = [&](const uint4& y, int64_t i) {
+      uint32_t at = 0;
+#pragma unroll
+      for (int e = 0; e < kPer; ++e) at |= !(pc.value(y, e) < floor_value) ? 1u << e : 0u;  // NaN too
+      while (at) {
+        const int e = __ffs(at) - 1;
+        at &= at - 1;
+        const uint32_t key = beam_key(pc.value_at(y, e));
+        if (key >= bound) beam_push(sh, key, i + e);
+      }
+    };
+    while (hits) {
+      const int v = __ffs(hits) - 1;
+      hits &= hits - 1;
+      gather(pc.load(v), pc.index(v));
+    }
+    if (edge_at >= 0 && key_top) gather(edge, edge_at * kPer - pc.mis);
     float s = (sum[0] + sum[1]) + (sum[2] + sum[3]);
 #pragma unroll
     for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
     if (lane == 0) sh.part[warp] = s;
     __syncthreads();
     if (sh.count > kBeamCap) beam_bisect(&sh, row_x, p.n, piece, p.pieces, p.k);
-    const int m = sh.count;
-    for (int i = tid; i < m; i += kBeamThreads) {
+    const int found = sh.count;
+    for (int i = tid; i < found; i += kBeamThreads) {
       const uint64_t e = sh.gathered[i];
       int above = 0;
-      for (int j = 0; j < m; ++j) above += sh.gathered[j] > e;
+#pragma unroll 4
+      for (int j = 0; j < found; ++j) above += sh.gathered[j] > e;
       if (above < p.k) list[above] = e;
     }
-    for (int i = m + tid; i < p.k; i += kBeamThreads) list[i] = 0;
+    for (int i = found + tid; i < p.k; i += kBeamThreads) list[i] = 0;
     if (tid == 0) {
       double t = 0.0;
 #pragma unroll
       for (int w = 0; w < kBeamThreads / 32; ++w) t += sh.part[w];
-      *sum_out = make_uint2(key_top, __float_as_uint(static_cast<float>(t)));
+      *sum_out = BeamSum{t * exp2(fix), key_top};
     }
   }
   __threadfence();

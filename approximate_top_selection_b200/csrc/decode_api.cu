@@ -157,10 +157,10 @@ BeamPlan plan_beam(int64_t batch, int beams, int64_t n, int k, int esz, const De
   BeamPlan pl;
   pl.pieces = beam_pieces(batch * beams, n, esz, dev);
   // as many sentences as have tickets and fit a grid and about 1 GB of lists
-  const int64_t row_bytes = static_cast<int64_t>(pl.pieces) * (8 + 8 * k) * beams;
+  const int64_t row_bytes = static_cast<int64_t>(pl.pieces) * (sizeof(BeamSum) + 8 * k) * beams;
   const int64_t fit = std::min<int64_t>((int64_t{1} << 30) / row_bytes, kMaxGridX / (static_cast<int64_t>(pl.pieces) * beams));
   pl.sentences = std::min(std::min(batch, static_cast<int64_t>(kBeamTickets)), std::max<int64_t>(fit, 1));
-  pl.sums = align_up(static_cast<size_t>(pl.sentences) * beams * pl.pieces * 8, 16);
+  pl.sums = static_cast<size_t>(pl.sentences) * beams * pl.pieces * sizeof(BeamSum);
   pl.lists = static_cast<size_t>(pl.sentences) * beams * pl.pieces * k * 8;
   return pl;
 }
@@ -182,7 +182,7 @@ int run_beam(const T* logits, const float* scores, int64_t batch, int beams, int
   BeamArgs a{logits, scores, n, beams, k, pl.pieces, 0, out_scores, out_parent, out_token, nullptr, nullptr, nullptr};
   unsigned char* base = static_cast<unsigned char*>(ws);
   a.tickets = reinterpret_cast<uint32_t*>(base);
-  a.sums = reinterpret_cast<uint2*>(base + kTicketBytes);
+  a.sums = reinterpret_cast<BeamSum*>(base + kTicketBytes);
   a.lists = reinterpret_cast<uint64_t*>(base + kTicketBytes + pl.sums);
   for (; a.first < batch; a.first += pl.sentences) {
     const int64_t rows = std::min(pl.sentences, batch - a.first) * beams;
