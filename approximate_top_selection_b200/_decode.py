@@ -13,7 +13,11 @@ import torch
 from ._binding import (TOPK_CACHE_BF16, TOPK_CACHE_E4M3, TopkCache, _check, _cuda, _OnDevice, _stream_handle,
                        load_library)
 
-_E4M3 = torch.float8_e4m3fn
+_E4M3, _BF16, _F32, _I32, _I64 = torch.float8_e4m3fn, torch.bfloat16, torch.float32, torch.int32, torch.int64
+
+# A step of a few microseconds on the GPU leaves the host as little time, so a
+# call first asks in a few cheap tests whether everything is as usual (get_device
+# is -1 on the CPU) and looks for what is wrong, test by test, only if not.
 
 
 def _cuda_strided(t: torch.Tensor, name: str, dtype, dims: int) -> None:
@@ -34,44 +38,103 @@ def _same_device(first: torch.Tensor, **others) -> None:
             raise ValueError("%s is on %s, not on %s" % (name, t.device, first.device))
 
 
-def _cache(data: torch.Tensor, scale, name: str) -> TopkCache:
-    """The C description of a cache tensor [pages, kv_heads, page_size, d]."""
+def _check_cache(data: torch.Tensor, scale, name: str) -> None:
     if isinstance(data, torch.Tensor) and data.dtype == _E4M3:
-        kind = TOPK_CACHE_E4M3
         _cuda_strided(data, name, _E4M3, 4)
         if scale is None:
             raise ValueError("%s is e4m3 and needs its scale" % name)
-        if not isinstance(scale, torch.Tensor) or not scale.is_cuda or scale.dtype != torch.float32:
+        if not isinstance(scale, torch.Tensor) or not scale.is_cuda or scale.dtype != _F32:
             raise TypeError("the scale of %s must be a float32 CUDA tensor" % name)
         if tuple(scale.shape) != tuple(data.shape[:3]):
             raise ValueError("the scale of %s must be [pages, kv_heads, page_size]" % name)
         _same_device(data, scale=scale)
     else:
-        kind = TOPK_CACHE_BF16
-        _cuda_strided(data, name, torch.bfloat16, 4)
+        _cuda_strided(data, name, _BF16, 4)
         if scale is not None:
             raise ValueError("%s is bfloat16 and takes no scale" % name)
-    pages, heads, page, d = data.shape
-    c = TopkCache(data.data_ptr(), scale.data_ptr() if scale is not None else None, pages, heads, page, d, kind,
-                  *data.stride()[:3], *(scale.stride() if scale is not None else (0, 0, 0)))
-    return c
 
 
-def _two_caches(k_cache, v_cache, k_scale, v_scale):
-    kc, vc = _cache(k_cache, k_scale, "k_cache"), _cache(v_cache, v_scale, "v_cache")
-    if k_cache.shape != v_cache.shape or k_cache.dtype != v_cache.dtype:
+def _cache(data: torch.Tensor, scale, name: str, dev: int):
+    """The C description of a cache tensor [pages, kv_heads, page_size, d] on
+    device `dev`, and its shape."""
+    try:
+        shape, strides, dtype = data.shape, data.stride(), data.dtype
+        good = data.get_device() == dev and len(shape) == 4 and strides[3] == 1
+        if dtype is _E4M3:
+            good = good and scale.get_device() == dev and scale.dtype is _F32 and scale.shape == shape[:3]
+        else:
+            good = good and dtype is _BF16 and scale is None
+    except (AttributeError, TypeError):
+        good = False
+    if not good:
+        _check_cache(data, scale, name)
+        if data.get_device() != dev:
+            raise ValueError("%s is on %s, not on cuda:%d" % (name, data.device, dev))
+    if scale is None:
+        return TopkCache(data.data_ptr(), None, *shape, TOPK_CACHE_BF16, *strides[:3], 0, 0, 0), shape
+    return TopkCache(data.data_ptr(), scale.data_ptr(), *shape, TOPK_CACHE_E4M3, *strides[:3], *scale.stride()), shape
+
+
+def _two_caches(k_cache, v_cache, k_scale, v_scale, dev):
+    (kc, ks), (vc, vs) = _cache(k_cache, k_scale, "k_cache", dev), _cache(v_cache, v_scale, "v_cache", dev)
+    if ks != vs or kc.type != vc.type:
         raise ValueError("k_cache and v_cache must have the same shape and dtype")
-    _same_device(k_cache, v_cache=v_cache)
-    return kc, vc
+    return kc, vc, ks
 
 
-def _table(block_table, seq_lens, batch):
-    _cuda_strided(block_table, "block_table", torch.int32, 2)
-    _cuda(seq_lens, "seq_lens", torch.int32)
+def _table(block_table, seq_lens, batch, dev):
+    """Checks the block table and the lengths; returns (stride, width) of the table."""
+    try:
+        (rows, width), (stride, inner) = block_table.shape, block_table.stride()
+        if (block_table.get_device() == dev and block_table.dtype is _I32 and inner == 1 and rows == batch and width > 0
+                and seq_lens.get_device() == dev and seq_lens.dtype is _I32 and seq_lens.shape == (batch,)
+                and (batch == 1 or seq_lens.stride() == (1,))):
+            return stride, width
+    except (AttributeError, TypeError, ValueError):
+        pass
+    _cuda_strided(block_table, "block_table", _I32, 2)
+    _cuda(seq_lens, "seq_lens", _I32)
     if block_table.shape[0] != batch or seq_lens.numel() != batch:
         raise ValueError("block_table must be [batch, width] and seq_lens [batch]")
     if block_table.shape[1] < 1:
         raise ValueError("block_table needs a column at least")
+    for name, t in (("block_table", block_table), ("seq_lens", seq_lens)):
+        if t.get_device() != dev:
+            raise ValueError("%s is on %s, not on cuda:%d" % (name, t.device, dev))
+    return block_table.stride(0), block_table.shape[1]
+
+
+def _device_of(t, name: str) -> int:
+    dev = t.get_device() if isinstance(t, torch.Tensor) else -1
+    if dev < 0:
+        raise TypeError("%s must be a CUDA tensor" % name)
+    return dev
+
+
+def _on(dev: int, stream, body, *args):
+    """body(*args, stream handle) with `dev` current and, if given, `stream` as torch's current stream."""
+    if stream is None and torch._C._cuda_getDevice() == dev:
+        return body(*args, torch._C._cuda_getCurrentRawStream(dev))
+    with _OnDevice(torch.device("cuda", dev), stream) as on:
+        return body(*args, _stream_handle(stream, on.index))
+
+
+def _out(t, shape, dtype, name: str, dev: int):
+    """A given output, checked, or a new one."""
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=_devices[dev])
+    _cuda(t, name, dtype)
+    if t.get_device() != dev:
+        raise ValueError("%s is on %s, not on cuda:%d" % (name, t.device, dev))
+    n = 1
+    for x in shape:
+        n *= x
+    if t.numel() != n:
+        raise ValueError("%s must hold %d elements" % (name, n))
+    return t
+
+
+_devices = [torch.device("cuda", i) for i in range(64)]
 
 
 # Workspace of paged_attention and topk_beam: one per (device, stream) for
@@ -82,17 +145,28 @@ def _table(block_table, seq_lens, batch):
 _ws_cache: dict = {}
 
 
-def _workspace(nbytes: int, device: torch.device, stream: int):
-    if nbytes == 0:
-        return None
-    if torch.cuda.is_current_stream_capturing():
-        return torch.zeros(nbytes, dtype=torch.uint8, device=device)
-    key = (device.index, stream)
-    ws = _ws_cache.get(key)
+def _workspace(nbytes: int, dev: int, stream: int):
+    if torch._C._cuda_isCurrentStreamCapturing():
+        return torch.zeros(nbytes, dtype=torch.uint8, device=_devices[dev])
+    ws = _ws_cache.get((dev, stream))
     if ws is None or ws.numel() < nbytes:
-        ws = torch.zeros(nbytes, dtype=torch.uint8, device=device)
-        _ws_cache[key] = ws
+        ws = torch.zeros(max(nbytes, 16), dtype=torch.uint8, device=_devices[dev])
+        _ws_cache[(dev, stream)] = ws
     return ws
+
+
+_ws_bytes: dict = {}
+
+
+def _workspace_bytes(query, *sizes) -> int:
+    """A workspace query for the current device, asked once per sizes."""
+    key = (torch._C._cuda_getDevice(), query, sizes)
+    n = _ws_bytes.get(key)
+    if n is None:
+        if len(_ws_bytes) > 4096:
+            _ws_bytes.clear()
+        n = _ws_bytes[key] = query(*sizes)
+    return n
 
 
 def _pointer(t):
@@ -120,48 +194,45 @@ def paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
     Returns out [batch, heads, d] bfloat16, or (out, lse [batch, heads]
     float32).  A head with nothing to attend to gives zeros and -inf.
     """
-    lib = load_library()
-    _cuda_strided(q, "q", torch.bfloat16, 3)
-    batch, heads, d = q.shape
-    if heads > 1 and q.stride(1) != d:
+    dev = _device_of(q, "q")
+    shape, strides = q.shape, q.stride()
+    if q.dtype is not _BF16 or len(shape) != 3 or strides[2] != 1:
+        _cuda_strided(q, "q", _BF16, 3)
+    batch, heads, d = shape
+    if heads > 1 and strides[1] != d:
         raise ValueError("the heads of q must be contiguous")
-    kc, vc = _two_caches(k_cache, v_cache, k_scale, v_scale)
-    if k_cache.shape[3] != d:
+    kc, vc, (_, kv_heads, _, cache_d) = _two_caches(k_cache, v_cache, k_scale, v_scale, dev)
+    if cache_d != d:
         raise ValueError("q and the caches disagree on d")
-    if heads % k_cache.shape[1]:
+    if kv_heads < 1 or heads % kv_heads:
         raise ValueError("heads must be a multiple of kv_heads")
-    _table(block_table, seq_lens, batch)
+    table_stride, width = _table(block_table, seq_lens, batch, dev)
     lists = c = 0
     if positions is not None:
-        _cuda(positions, "positions", torch.int32)
+        _cuda(positions, "positions", _I32)
+        _same_device(q, positions=positions)
         if positions.dim() != 3 or positions.shape[0] != batch:
             raise ValueError("positions must be [batch, lists, c]")
         lists, c = positions.shape[1:]
-        if lists < 1 or c < 1 or lists % k_cache.shape[1] or heads % lists:
+        if lists < 1 or c < 1 or lists % kv_heads or heads % lists:
             raise ValueError("positions needs c >= 1 and lists a multiple of kv_heads that divides heads")
-    _same_device(q, k_cache=k_cache, block_table=block_table, seq_lens=seq_lens, positions=positions, out=out,
-                 out_lse=out_lse, workspace=workspace)
-    with _OnDevice(q.device, stream) as on:
-        sh = _stream_handle(stream, on.index)
-        if out is None:
-            out = torch.empty(batch, heads, d, dtype=torch.bfloat16, device=q.device)
-        _cuda(out, "out", torch.bfloat16)
-        if out_lse is None and return_lse:
-            out_lse = torch.empty(batch, heads, dtype=torch.float32, device=q.device)
-        if out_lse is not None:
-            _cuda(out_lse, "out_lse", torch.float32)
-        if out.numel() != q.numel() or (out_lse is not None and out_lse.numel() != batch * heads):
-            raise ValueError("out must hold batch*heads*d elements and out_lse batch*heads")
-        ws = workspace
+    if workspace is not None:
+        _same_device(q, workspace=workspace)
+
+    def body(out, out_lse, ws, sh):
+        out = _out(out, shape, _BF16, "out", dev)
+        if return_lse or out_lse is not None:
+            out_lse = _out(out_lse, (batch, heads), _F32, "out_lse", dev)
         if ws is None:
-            ws = _workspace(paged_attention_workspace_bytes(batch, heads, lists, d), q.device, sh)
-        st = lib.paged_attention(
-            q.data_ptr(), q.stride(0), batch, heads, ctypes.byref(kc), ctypes.byref(vc), block_table.data_ptr(),
-            block_table.stride(0), block_table.shape[1], seq_lens.data_ptr(), _pointer(positions), lists, c,
-            d ** -0.5 if scale is None else float(scale), out.data_ptr(), _pointer(out_lse), _pointer(ws),
-            ws.numel() if ws is not None else 0, sh)
-    _check(st, "paged_attention")
-    return (out, out_lse) if return_lse else out
+            ws = _workspace(_workspace_bytes(paged_attention_workspace_bytes, 1, 1, 0, d), dev, sh)
+        _check(load_library().paged_attention(
+            q.data_ptr(), strides[0], batch, heads, ctypes.byref(kc), ctypes.byref(vc), block_table.data_ptr(),
+            table_stride, width, seq_lens.data_ptr(), _pointer(positions), lists, c,
+            d ** -0.5 if scale is None else scale, out.data_ptr(), _pointer(out_lse), ws.data_ptr(), ws.numel(), sh),
+            "paged_attention")
+        return (out, out_lse) if return_lse else out
+
+    return _on(dev, stream, body, out, out_lse, workspace)
 
 
 def cache_write(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, slots: torch.Tensor,
@@ -174,21 +245,34 @@ def cache_write(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cache
     must be distinct.  Caches and scales as in paged_attention; an e4m3 row
     gets the smallest power-of-two scale that holds it.
     """
-    lib = load_library()
-    _cuda_strided(k, "k", torch.bfloat16, 3)
-    _cuda_strided(v, "v", torch.bfloat16, 3)
-    kc, vc = _two_caches(k_cache, v_cache, k_scale, v_scale)
-    if k.shape != v.shape or tuple(k.shape[1:]) != (k_cache.shape[1], k_cache.shape[3]):
+    dev = _device_of(k, "k")
+    kc, vc, cache_shape = _two_caches(k_cache, v_cache, k_scale, v_scale, dev)
+    shape, ks = k.shape, k.stride()
+    try:
+        vs = v.stride()
+        good = (k.dtype is _BF16 and v.dtype is _BF16 and len(shape) == 3 and ks[2] == 1 and vs[2] == 1
+                and v.shape == shape and v.get_device() == dev and slots.get_device() == dev and slots.dtype is _I64
+                and slots.shape == shape[:1] and slots.is_contiguous())
+    except (AttributeError, TypeError, IndexError):
+        good = False
+    if not good:
+        _cuda_strided(k, "k", _BF16, 3)
+        _cuda_strided(v, "v", _BF16, 3)
+        if v.shape != shape:
+            raise ValueError("k and v must have the same shape")
+        _cuda(slots, "slots", _I64)
+        if slots.dim() != 1 or slots.numel() != shape[0]:
+            raise ValueError("slots must be [tokens]")
+        _same_device(k, v=v, slots=slots)
+        vs = v.stride()
+    if shape[1] != cache_shape[1] or shape[2] != cache_shape[3]:
         raise ValueError("k and v must be [tokens, kv_heads, d]")
-    _cuda(slots, "slots", torch.int64)
-    if slots.dim() != 1 or slots.numel() != k.shape[0]:
-        raise ValueError("slots must be [tokens]")
-    _same_device(k, v=v, k_cache=k_cache, slots=slots)
-    with _OnDevice(k.device, stream) as on:
-        sh = _stream_handle(stream, on.index)
-        st = lib.cache_write(k.data_ptr(), k.stride(0), k.stride(1), v.data_ptr(), v.stride(0), v.stride(1),
-                             k.shape[0], ctypes.byref(kc), ctypes.byref(vc), slots.data_ptr(), sh)
-    _check(st, "cache_write")
+
+    def body(sh):
+        _check(load_library().cache_write(k.data_ptr(), ks[0], ks[1], v.data_ptr(), vs[0], vs[1], shape[0],
+                                          ctypes.byref(kc), ctypes.byref(vc), slots.data_ptr(), sh), "cache_write")
+
+    _on(dev, stream, body)
 
 
 def cache_read(cache: torch.Tensor, block_table: torch.Tensor, seq_lens: torch.Tensor, n: int, *, scale=None,
@@ -198,23 +282,21 @@ def cache_read(cache: torch.Tensor, block_table: torch.Tensor, seq_lens: torch.T
     Rows behind a sequence's end are zeros.  `out.view(-1, n, d)` is the key
     matrix per row that score_topk and score_rerank take.
     """
-    lib = load_library()
-    c = _cache(cache, scale, "cache")
+    dev = _device_of(cache, "cache")
+    c, (_, kv_heads, _, d) = _cache(cache, scale, "cache", dev)
     batch = seq_lens.numel() if isinstance(seq_lens, torch.Tensor) else 0
-    _table(block_table, seq_lens, batch)
-    _same_device(cache, block_table=block_table, seq_lens=seq_lens, out=out)
-    shape = (batch, cache.shape[1], int(n), cache.shape[3])
-    with _OnDevice(cache.device, stream) as on:
-        sh = _stream_handle(stream, on.index)
-        if out is None:
-            out = torch.empty(shape, dtype=torch.bfloat16, device=cache.device)
-        _cuda(out, "out", torch.bfloat16)
-        if tuple(out.shape) != shape:
-            raise ValueError("out must be [batch, kv_heads, n, d]")
-        st = lib.cache_read(ctypes.byref(c), block_table.data_ptr(), block_table.stride(0), block_table.shape[1],
-                            seq_lens.data_ptr(), batch, int(n), out.data_ptr(), sh)
-    _check(st, "cache_read")
-    return out
+    table_stride, width = _table(block_table, seq_lens, batch, dev)
+    n = int(n)
+    if out is not None and tuple(out.shape) != (batch, kv_heads, n, d):
+        raise ValueError("out must be [batch, kv_heads, n, d]")
+
+    def body(out, sh):
+        out = _out(out, (batch, kv_heads, max(n, 0), d), _BF16, "out", dev)
+        _check(load_library().cache_read(ctypes.byref(c), block_table.data_ptr(), table_stride, width,
+                                         seq_lens.data_ptr(), batch, n, out.data_ptr() or None, sh), "cache_read")
+        return out
+
+    return _on(dev, stream, body, out)
 
 
 def topk_beam_workspace_bytes(batch: int, beams: int, n: int, k: int) -> int:
@@ -232,34 +314,38 @@ def topk_beam(logits: torch.Tensor, beam_scores: torch.Tensor, k: int, *, out_sc
     parents int32, tokens int32), each [batch, k], best first, padded with
     -inf, -1, -1.
     """
-    lib = load_library()
-    bf16 = isinstance(logits, torch.Tensor) and logits.dtype == torch.bfloat16
-    _cuda(logits, "logits", torch.bfloat16 if bf16 else torch.float32)
-    _cuda(beam_scores, "beam_scores", torch.float32)
-    if logits.dim() != 3 or tuple(beam_scores.shape) != tuple(logits.shape[:2]):
-        raise ValueError("logits must be [batch, beams, n] and beam_scores [batch, beams]")
-    _same_device(logits, beam_scores=beam_scores, out_scores=out_scores, out_parent=out_parent, out_token=out_token,
-                 workspace=workspace)
+    dev = _device_of(logits, "logits")
+    bf16 = logits.dtype is _BF16
+    try:
+        good = ((bf16 or logits.dtype is _F32) and logits.dim() == 3 and logits.is_contiguous()
+                and beam_scores.get_device() == dev and beam_scores.dtype is _F32
+                and beam_scores.shape == logits.shape[:2] and beam_scores.is_contiguous())
+    except (AttributeError, TypeError):
+        good = False
+    if not good:
+        _cuda(logits, "logits", _BF16 if bf16 else _F32)
+        _cuda(beam_scores, "beam_scores", _F32)
+        if logits.dim() != 3 or tuple(beam_scores.shape) != tuple(logits.shape[:2]):
+            raise ValueError("logits must be [batch, beams, n] and beam_scores [batch, beams]")
+        _same_device(logits, beam_scores=beam_scores)
+    if workspace is not None:
+        _same_device(logits, workspace=workspace)
     batch, beams, n = logits.shape
-    with _OnDevice(logits.device, stream) as on:
-        sh = _stream_handle(stream, on.index)
-        outs = []
-        for t, name, dtype in ((out_scores, "out_scores", torch.float32), (out_parent, "out_parent", torch.int32),
-                               (out_token, "out_token", torch.int32)):
-            if t is None:
-                t = torch.empty(batch, k, dtype=dtype, device=logits.device)
-            _cuda(t, name, dtype)
-            if t.numel() != batch * k:
-                raise ValueError("outputs must hold batch*k elements")
-            outs.append(t)
-        ws = workspace
+
+    def body(out_scores, out_parent, out_token, ws, sh):
+        shape = (batch, max(k, 0))
+        out_scores = _out(out_scores, shape, _F32, "out_scores", dev)
+        out_parent = _out(out_parent, shape, _I32, "out_parent", dev)
+        out_token = _out(out_token, shape, _I32, "out_token", dev)
         if ws is None:
-            ws = _workspace(topk_beam_workspace_bytes(batch, beams, n, k), logits.device, sh)
+            ws = _workspace(_workspace_bytes(topk_beam_workspace_bytes, batch, beams, n, k), dev, sh)
+        lib = load_library()
         fn = lib.topk_beam_bf16 if bf16 else lib.topk_beam
-        st = fn(logits.data_ptr(), beam_scores.data_ptr(), batch, beams, n, k, *(t.data_ptr() for t in outs),
-                _pointer(ws), ws.numel() if ws is not None else 0, sh)
-    _check(st, "topk_beam")
-    return tuple(outs)
+        _check(fn(logits.data_ptr(), beam_scores.data_ptr(), batch, beams, n, k, out_scores.data_ptr(),
+                  out_parent.data_ptr(), out_token.data_ptr(), ws.data_ptr(), ws.numel(), sh), "topk_beam")
+        return out_scores, out_parent, out_token
+
+    return _on(dev, stream, body, out_scores, out_parent, out_token, workspace)
 
 
 def beam_reorder(states, parents: torch.Tensor, *, out=None, stream=None):
@@ -270,38 +356,46 @@ def beam_reorder(states, parents: torch.Tensor, *, out=None, stream=None):
     with [batch, k, ...]: row (b, j) is row (b, parents[b, j]), zeros where
     that is -1.  `out` (of the same form) must not overlap the states.
     """
-    lib = load_library()
     one = isinstance(states, torch.Tensor)
     src = [states] if one else list(states)
-    _cuda(parents, "parents", torch.int32)
+    dev = _device_of(parents, "parents")
+    if parents.dtype is not _I32 or not parents.is_contiguous():
+        _cuda(parents, "parents", _I32)
     if not src or parents.dim() != 2:
         raise ValueError("states needs a tensor at least and parents must be [batch, k]")
-    for t in src:
-        _cuda(t, "states", t.dtype if isinstance(t, torch.Tensor) else None)
-        if t.dim() < 2 or tuple(t.shape[:2]) != tuple(src[0].shape[:2]) or t.shape[0] != parents.shape[0]:
-            raise ValueError("every state must be [batch, beams, ...]")
-        if t.numel() == 0:
-            raise ValueError("states must not be empty")
-        _same_device(parents, states=t)
     batch, k = parents.shape
-    beams = src[0].shape[1]
-    with _OnDevice(parents.device, stream) as on:
-        sh = _stream_handle(stream, on.index)
-        if out is None:
-            dst = [torch.empty((batch, k) + tuple(t.shape[2:]), dtype=t.dtype, device=t.device) for t in src]
-        else:
-            dst = [out] if isinstance(out, torch.Tensor) else list(out)
-            if len(dst) != len(src):
-                raise ValueError("out needs one tensor per state")
-            for t, o in zip(src, dst):
-                _cuda(o, "out", t.dtype)
-                _same_device(t, out=o)
-                if tuple(o.shape) != (batch, k) + tuple(t.shape[2:]):
-                    raise ValueError("out must be [batch, k, ...]")
+    beams = 0
+    sizes = []
+    for t in src:
+        if not isinstance(t, torch.Tensor) or t.get_device() != dev or not t.is_contiguous():
+            _cuda(t, "states", t.dtype if isinstance(t, torch.Tensor) else None)
+            _same_device(parents, states=t)
+        shape = t.shape
+        beams = beams or (shape[1] if len(shape) > 1 else 0)
+        if len(shape) < 2 or shape[0] != batch or shape[1] != beams:
+            raise ValueError("every state must be [batch, beams, ...]")
+        n = t.numel()
+        if n == 0:
+            raise ValueError("states must not be empty")
+        sizes.append(n // (batch * beams) * t.element_size())
+    if out is not None:
+        out = [out] if isinstance(out, torch.Tensor) else list(out)
+        if len(out) != len(src):
+            raise ValueError("out needs one tensor per state")
+        for t, o in zip(src, out):
+            _cuda(o, "out", t.dtype)
+            _same_device(parents, out=o)
+            if tuple(o.shape) != (batch, k) + tuple(t.shape[2:]):
+                raise ValueError("out must be [batch, k, ...]")
+
+    def body(dst, sh):
+        if dst is None:
+            dst = [t.new_empty((batch, k) + t.shape[2:]) if k != beams else torch.empty_like(t) for t in src]
         m = len(src)
         pointers = ctypes.c_void_p * m
-        size = (ctypes.c_int64 * m)(*(t.numel() // (batch * beams) * t.element_size() for t in src))
-        st = lib.beam_reorder(pointers(*(t.data_ptr() for t in src)), pointers(*(t.data_ptr() for t in dst)), size, m,
-                              batch, beams, k, parents.data_ptr(), sh)
-    _check(st, "beam_reorder")
-    return dst[0] if one else dst
+        _check(load_library().beam_reorder(pointers(*[t.data_ptr() for t in src]), pointers(*[t.data_ptr() for t in dst]),
+                                           (ctypes.c_int64 * m)(*sizes), m, batch, beams, k, parents.data_ptr(), sh),
+               "beam_reorder")
+        return dst[0] if one else dst
+
+    return _on(dev, stream, body, out)
