@@ -143,11 +143,14 @@ _devices = [torch.device("cuda", i) for i in range(64)]
 # the graph's memory instead, so that graphs (which may be replayed on other
 # streams, side by side) share none.
 _ws_cache: dict = {}
+_WS_ZERO = 16384  # TOPK_DECODE_TICKET_BYTES
 
 
 def _workspace(nbytes: int, dev: int, stream: int):
     if torch._C._cuda_isCurrentStreamCapturing():
-        return torch.zeros(nbytes, dtype=torch.uint8, device=_devices[dev])
+        ws = torch.empty(max(nbytes, _WS_ZERO), dtype=torch.uint8, device=_devices[dev])
+        ws[:_WS_ZERO].zero_()
+        return ws
     ws = _ws_cache.get((dev, stream))
     if ws is None or ws.numel() < nbytes:
         ws = torch.zeros(max(nbytes, 16), dtype=torch.uint8, device=_devices[dev])

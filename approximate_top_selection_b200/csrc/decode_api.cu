@@ -20,7 +20,7 @@ namespace tk {
 namespace {
 
 // The part of a workspace that is zero between calls, of every operator.
-constexpr size_t kTicketBytes = 16384;
+constexpr size_t kTicketBytes = TOPK_DECODE_TICKET_BYTES;
 static_assert(kTicketBytes >= 4 * kAttendMaxCtas && kTicketBytes >= 4 * kBeamTickets, "tickets");
 
 constexpr int kMaxReorder = 256;
@@ -87,18 +87,18 @@ size_t attend_workspace(int d, const DeviceInfo& dev) {
   return kTicketBytes + static_cast<size_t>(ctas) * 2 * attend_part_floats(d) * 4;
 }
 
-template <int D, bool kE4m3, bool kFull>
+template <int D, bool kE4m3, int NT>
 int launch_attend_rows(AttendArgs& a, const DeviceInfo& dev, cudaStream_t st) {
-  using S = AttendShape<D, kE4m3>;
+  using S = AttendShape<D, kE4m3, NT>;
   if (S::kSmem > dev.max_smem_optin) return TOPK_EUNSUPPORTED;
   int rc, per_sm = 0;
-  if ((rc = occupancy(paged_attention_kernel<D, kE4m3, kFull>, kAttendThreads, S::kSmem, &per_sm))) return rc;
+  if ((rc = occupancy(paged_attention_kernel<D, kE4m3, NT>, kAttendThreads, S::kSmem, &per_sm))) return rc;
   const int64_t most = a.positions ? a.c : a.tab.capacity;
   const int64_t granules = (most + S::kGranule - 1) / S::kGranule;
   const int64_t units = static_cast<int64_t>(a.lists) * a.row_tiles * a.tab.batch;
   int64_t ctas = std::min(std::min(per_sm, kAttendCtasPerSm) * dev.sms, kAttendMaxCtas);
   if (granules <= ctas / units) ctas = std::max<int64_t>(1, granules * units);
-  return launch_pdl(paged_attention_kernel<D, kE4m3, kFull>, dim3(static_cast<unsigned>(ctas)), dim3(kAttendThreads),
+  return launch_pdl(paged_attention_kernel<D, kE4m3, NT>, dim3(static_cast<unsigned>(ctas)), dim3(kAttendThreads),
                     S::kSmem, st, a);
 }
 
@@ -107,7 +107,7 @@ int launch_attend(AttendArgs& a, const DeviceInfo& dev, cudaStream_t st) {
   const int group = a.heads / a.lists;
   a.row_tiles = (group + 15) / 16;
   if (static_cast<int64_t>(a.lists) * a.row_tiles > kMaxN / a.tab.batch) return TOPK_EUNSUPPORTED;
-  return group > 8 ? launch_attend_rows<D, kE4m3, true>(a, dev, st) : launch_attend_rows<D, kE4m3, false>(a, dev, st);
+  return group > 8 ? launch_attend_rows<D, kE4m3, 2>(a, dev, st) : launch_attend_rows<D, kE4m3, 1>(a, dev, st);
 }
 
 template <int D, bool kE4m3>
@@ -238,6 +238,12 @@ int paged_attention(const uint16_t* q, int64_t q_stride, int64_t batch, int head
   a.parts = reinterpret_cast<float*>(static_cast<unsigned char*>(workspace) + kTicketBytes);
   a.same_strides = a.k.page_stride == a.v.page_stride && a.k.head_stride == a.v.head_stride &&
                    a.k.token_stride == a.v.token_stride;
+  // t / page_size for t < 2^31 by a multiplication: 2^shift / page_size rounded up, shift = 31 + ceil(log2 page_size)
+  a.page_shift = 31;
+  while ((1LL << (a.page_shift - 31)) < k_cache->page_size) ++a.page_shift;
+  a.page_magic = static_cast<uint32_t>(((static_cast<unsigned __int128>(1) << a.page_shift) + k_cache->page_size - 1) /
+                                       static_cast<unsigned>(k_cache->page_size));
+  a.grouped = !positions && k_cache->page_size % 16 == 0;
   a.q = q;
   a.q_stride = q_stride;
   a.positions = positions;

@@ -6,10 +6,12 @@
 // m of the scores (in units of log2), l = sum 2^(s_j - m) and O = sum
 // 2^(s_j - m) V_j; two such triples join as (max m, ...) with the factors
 // 2^(m_a - m).  A key-value head is read once for all query heads that share
-// it: up to 16 of them are the 16 rows of m16n8k16 matrix products (S = Q K^T,
-// O += P V), so the work per cached byte stays far below the memory's pace:
-// 4 * 16 flops per element of K and V, about 100 TFLOP/s at full bandwidth.
-// The kernel is bound by reading K and V from HBM.
+// it, eight or sixteen at a time: they are the columns of the matrix products
+// S^T = K Q^T (16 keys x 8 heads) and O^T += V^T P^T (16 columns of V x 8
+// heads), so that a head that shares its keys with none wastes seven eighths of
+// the small operand, not of the large one.  16 flops per element of K and V and
+// group of eight heads: 51 TFLOP/s of bf16 at full bandwidth.  The kernel is
+// bound by reading K and V from HBM.
 //
 // Work: a unit is (sequence, list of query heads); its tokens are cut into
 // granules of 4 * KT tokens, one tile of KT keys per warp.  All granules of
@@ -36,6 +38,8 @@ struct AttendArgs {
   const int32_t* positions;  // null, or [batch][lists][c]
   int heads, lists, c;
   int row_tiles;      // groups of 16 query heads per list
+  uint32_t page_magic, page_shift;  // t / page_size = (t * page_magic) >> page_shift for 0 <= t < 2^31
+  bool grouped;       // no positions, and 16 | page_size: 16 tokens from a multiple of 16 on share a page
   bool same_strides;  // k and v have equal strides
   float scale_log2;   // softmax scale * log2(e)
   uint16_t* out;      // [batch][heads][d] bf16
@@ -50,7 +54,7 @@ constexpr int kAttendMaxCtas = 1024;
 
 __host__ __device__ constexpr int attend_part_floats(int d) { return 16 * (d + 2); }
 
-template <int D, bool kE4m3>
+template <int D, bool kE4m3, int NT>
 struct AttendShape {
   static constexpr int kRowBytes = D * (kE4m3 ? 1 : 2);
   static constexpr int kChunks = kRowBytes / 16;
@@ -59,18 +63,24 @@ struct AttendShape {
   static constexpr int kTileBytes = kKeys * kRowBytes;               // K or V
   static constexpr int kScaleBytes = kE4m3 ? 2 * kKeys * 4 : 0;
   static constexpr int kStageBytes = 2 * kTileBytes + kScaleBytes;
-  static constexpr int kStages = D == 64 && kE4m3 ? 6 : 3;
-  static constexpr int kCtasPerSm = D == 256 && !kE4m3 ? 1 : 2;
-  static constexpr bool kQShared = D == 256;  // Q fragments in shared memory (64 registers otherwise)
-  static constexpr int kJoinCols = D == 128 ? 128 : 64;
-  static constexpr int kJoinPitch = kJoinCols + 8;  // floats; spreads a column's rows over the banks
+  static constexpr bool kQShared = D == 256 && NT == 2;  // Q fragments in shared memory (64 registers otherwise)
+  // 8 KB a tile: three stages of four warps and two CTAs fill an SM's shared memory
+  static constexpr int kCtasPerSm = D == 256 && (!kE4m3 || NT == 2) ? 1 : 2;
+  static constexpr int kStages = D == 64 && kE4m3 ? 6 : D == 256 && kE4m3 && NT == 2 ? 5 : 3;
+  static constexpr int kJoinFloats = 2304;
   // shared memory: [warps][stages] tiles, join buffer, Q fragments, (m, l) per warp and joined, valid masks, plan
   static constexpr int kOffJoin = kAttendWarps * kStages * kStageBytes;
-  static constexpr int kOffQ = kOffJoin + 16 * kJoinPitch * 4;
-  static constexpr int kOffMl = kOffQ + (kQShared ? D / 16 * 512 : 0);
+  static constexpr int kOffQ = kOffJoin + kJoinFloats * 4;
+  static constexpr int kOffMl = kOffQ + (kQShared ? 8192 : 0);
   static constexpr int kOffValid = kOffMl + (kAttendWarps + 1) * 32 * 4;
   static constexpr int kOffPlan = kOffValid + kAttendWarps * kStages * 4;
   static constexpr int kSmem = (kOffPlan + 64 + 127) / 128 * 128;
+  static_assert(kOffPlan % 8 == 0, "plan alignment");
+  // Columns of O joined at a time: 4 warps x rows x (columns + 4) floats fit
+  // the buffer; the 4 spread a lane quad's heads over the banks.
+  static __device__ __forceinline__ int join_columns(int rows) {
+    return min(D, (kJoinFloats / (kAttendWarps * rows) - 4) & ~15);
+  }
 };
 
 // ---------------------------------------------------------------- instructions
@@ -114,6 +124,19 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
+__device__ __forceinline__ void mma16832_e4m3(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// Transposes an 8x8 matrix of 16-bit values held across the warp.
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+  return r;
+}
 __device__ __forceinline__ float exp2_fast(float x) {  // 2^x, relative error below 2^-22
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -124,9 +147,16 @@ __device__ __forceinline__ uint32_t floats_to_f16x2(float a, float b) {
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
   return r;
 }
-__device__ __forceinline__ float quad_max(float x) {
-  x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
-  return fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
+// Over the eight lanes of a column (those of equal lane % 4).
+__device__ __forceinline__ float column_max(float x) {
+#pragma unroll
+  for (int d = 4; d < 32; d <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, d));
+  return x;
+}
+__device__ __forceinline__ float column_sum(float x) {
+#pragma unroll
+  for (int d = 4; d < 32; d <<= 1) x += __shfl_xor_sync(0xffffffffu, x, d);
+  return x;
 }
 __device__ __forceinline__ float finite_or_zero(float m) { return m == __int_as_float(0xff800000) ? 0.0f : m; }
 
@@ -144,14 +174,14 @@ __device__ __forceinline__ int granules_of(int count) {
   return static_cast<int>((static_cast<uint32_t>(count) + kGranule - 1) / kGranule);
 }
 
-template <int D, bool kE4m3>
+template <int kGranule>
 __device__ __forceinline__ void cursor_enter(const AttendArgs& p, AttendCursor& u) {
   u.count = p.positions ? p.c : seq_length(p.tab, u.b);
-  u.granules = granules_of<AttendShape<D, kE4m3>::kGranule>(u.count);
+  u.granules = granules_of<kGranule>(u.count);
 }
 
 // To the next granule; past the last one `b` is tab.batch and nothing may be read.
-template <int D, bool kE4m3>
+template <int kGranule>
 __device__ __forceinline__ void cursor_next(const AttendArgs& p, AttendCursor& u) {
   if (++u.at < u.granules) return;
   u.at = 0;
@@ -163,95 +193,139 @@ __device__ __forceinline__ void cursor_next(const AttendArgs& p, AttendCursor& u
       u.count = 0;
       return;
     }
-    cursor_enter<D, kE4m3>(p, u);
+    cursor_enter<kGranule>(p, u);
   } while (u.granules == 0);
 }
 
 // ---------------------------------------------------------------- one warp's state
-template <int D, bool kE4m3, bool kFull>
+// A lane's place in the products: g = lane / 4, t = lane % 4.  Scores: keys g
+// and g + 8 of each 16, heads 2t and 2t + 1 of each 8.  O^T: columns of V by g,
+// the same heads.
+template <int D, bool kE4m3, int NT>
 struct AttendWarp {
-  using S = AttendShape<D, kE4m3>;
-  static constexpr int kTiles = S::kKeys / 8;  // score tiles of 8 keys
-  static constexpr int kRows = kFull ? 2 : 1;  // rows g and g + 8 of a lane
+  using S = AttendShape<D, kE4m3, NT>;
+  static constexpr int kGroups = S::kKeys / 16;
+  static constexpr int kSteps = kE4m3 ? D / 32 : D / 16;  // of the product over d
+  static constexpr int kQWords = kE4m3 ? 4 : 2;           // registers of Q per step and 8 heads
 
-  float o[D / 8][4];
-  float m[2], l[2];
-  float f[2];        // e4m3: O holds sum w_j V8_j / f, with w_j = 2^(s_j - m) * vscale_j
-  uint32_t q[S::kQShared ? 1 : D / 16][4];
-  float row_scale[2];  // score in log2 units per unit of the product
+  float o[NT][D / 16][4];
+  float m[NT][2], l[NT][2];
+  float f[NT][2];  // e4m3: O holds sum w_j V8_j / f, with w_j = 2^(s_j - m) * vscale_j
+  uint32_t q[NT][S::kQShared ? 1 : kSteps][kQWords];
+  float head_scale[NT][2];  // score in log2 units per unit of the product
 
   __device__ __forceinline__ void reset() {
 #pragma unroll
-    for (int j = 0; j < D / 8; ++j)
+    for (int n = 0; n < NT; ++n) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) o[j][i] = 0.0f;
+      for (int j = 0; j < D / 16; ++j)
 #pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      m[r] = __int_as_float(0xff800000);
-      l[r] = 0.0f;
-      f[r] = 0.0f;
+        for (int i = 0; i < 4; ++i) o[n][j][i] = 0.0f;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        m[n][h] = __int_as_float(0xff800000);
+        l[n][h] = 0.0f;
+        f[n][h] = 0.0f;
+      }
     }
   }
 
-  // Fragments of the 16 query rows (zeros behind `rows`).  Beside e4m3 keys
-  // the products run in f16: a row is scaled by the power of two that brings
-  // its largest finite value into [2^14, 2^15), where rounding to f16 moves a
-  // value by at most 2^-25 (below 2^-39 of that largest one).
+  // Fragments of the query heads (zeros behind `rows`).  Beside e4m3 keys the
+  // product runs in e4m3 too, on the codes as they lie in the cache: a head is
+  // scaled by the power of two that brings its largest finite value into
+  // [128, 256) and split into two codes, q = a + b / 32.  a keeps 4 significant
+  // bits and b the next 4, all a bf16 value has; what is below 2^-14 of the
+  // head's largest value keeps an absolute error of 2^-22 of that value, as
+  // much as the fp32 sum itself.  (An infinity in q counts as NaN there.)
   __device__ __forceinline__ void load_q(const AttendArgs& p, const uint16_t* q0, int rows, uint4* shared, int warp) {
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-    float mul[2] = {1.0f, 1.0f};
-    row_scale[0] = row_scale[1] = p.scale_log2;
-    if constexpr (kE4m3) {
 #pragma unroll
-      for (int r = 0; r < kRows; ++r) {
+    for (int n = 0; n < NT; ++n) {
+      const bool live = n * 8 + g < rows;
+      const uint16_t* row = q0 + static_cast<int64_t>(n * 8 + g) * D;
+      head_scale[n][0] = head_scale[n][1] = p.scale_log2;
+      if constexpr (!kE4m3) {
+#pragma unroll
+        for (int ks = 0; ks < kSteps; ++ks) {
+          if (S::kQShared && ks % kAttendWarps != warp) continue;
+          const uint32_t* src = reinterpret_cast<const uint32_t*>(row + ks * 16);
+          const uint32_t b0 = live ? __ldg(src + t) : 0u, b1 = live ? __ldg(src + t + 4) : 0u;
+          if constexpr (S::kQShared) {
+            reinterpret_cast<uint2*>(shared)[(ks * NT + n) * 32 + lane] = make_uint2(b0, b1);
+          } else {
+            q[n][ks][0] = b0;
+            q[n][ks][1] = b1;
+          }
+        }
+      } else {
         uint32_t top = 0;
-        if (g + 8 * r < rows) {
-          const uint2* src = reinterpret_cast<const uint2*>(q0 + static_cast<int64_t>(g + 8 * r) * D) + t;
 #pragma unroll 4
-          for (int ks = 0; ks < D / 16; ++ks) {
-            const uint2 w = __ldg(src + ks * 4);
-            const uint32_t h[4] = {w.x << 16, w.x, w.y << 16, w.y};
+        for (int ks = 0; ks < D / 16; ++ks) {
+          const uint2 w = live ? __ldg(reinterpret_cast<const uint2*>(row + ks * 16) + t) : make_uint2(0, 0);
+          const uint32_t h[4] = {w.x << 16, w.x, w.y << 16, w.y};
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const uint32_t v = h[i] & 0x7fff0000u;
-              if (v < 0x7f800000u) top = max(top, v);
-            }
+          for (int i = 0; i < 4; ++i) {
+            const uint32_t v = h[i] & 0x7fff0000u;
+            if (v < 0x7f800000u) top = max(top, v);
           }
         }
         top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
         top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        float mul = 1.0f, scale = p.scale_log2;
         if (top) {
-          int e = 14 - (static_cast<int>(top >> 23) - 127);
+          int e = 7 - (static_cast<int>(top >> 23) - 127);
           e = min(max(e, -126), 126);
-          mul[r] = power_of_two(e);
-          row_scale[r] = p.scale_log2 * power_of_two(-e);
+          mul = power_of_two(e);
+          scale = p.scale_log2 * power_of_two(-e);
         }
-      }
-    }
+        head_scale[n][0] = __shfl_sync(0xffffffffu, scale, 8 * t);
+        head_scale[n][1] = __shfl_sync(0xffffffffu, scale, 8 * t + 4);
 #pragma unroll
-    for (int ks = 0; ks < D / 16; ++ks) {
-      if (S::kQShared && ks % kAttendWarps != warp) continue;
-      uint32_t a[4] = {0, 0, 0, 0};
+        for (int ks = 0; ks < kSteps; ++ks) {
+          if (S::kQShared && ks % kAttendWarps != warp) continue;
+          uint32_t code[4];
 #pragma unroll
-      for (int r = 0; r < kRows; ++r) {
-        if (g + 8 * r < rows) {
-          const uint16_t* row = q0 + static_cast<int64_t>(g + 8 * r) * D + ks * 16;
-          if constexpr (kE4m3) {
-            const uint2 w = __ldg(reinterpret_cast<const uint2*>(row) + t);
-            a[r] = floats_to_f16x2(__uint_as_float(w.x << 16) * mul[r], __uint_as_float(w.x & 0xffff0000u) * mul[r]);
-            a[2 + r] = floats_to_f16x2(__uint_as_float(w.y << 16) * mul[r], __uint_as_float(w.y & 0xffff0000u) * mul[r]);
+          for (int half = 0; half < 2; ++half) {  // 16 values each, four of them this lane's
+            const uint2 w = live ? __ldg(reinterpret_cast<const uint2*>(row + ks * 32 + half * 16) + t) : make_uint2(0, 0);
+            float v[4] = {__uint_as_float(w.x << 16) * mul, __uint_as_float(w.x & 0xffff0000u) * mul,
+                          __uint_as_float(w.y << 16) * mul, __uint_as_float(w.y & 0xffff0000u) * mul};
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              if (!(fabsf(v[i]) < __int_as_float(0x7f800000))) v[i] = __int_as_float(0x7fffffff);
+            const uint32_t a01 = floats_to_e4m3x2(v[0], v[1]), a23 = floats_to_e4m3x2(v[2], v[3]);
+            const float2 f01 = f16x2_to_float2(e4m3x2_to_f16x2(a01)), f23 = f16x2_to_float2(e4m3x2_to_f16x2(a23));
+            code[half] = a01 | (a23 << 16);
+            code[2 + half] = floats_to_e4m3x2((v[0] - f01.x) * 32.0f, (v[1] - f01.y) * 32.0f) |
+                             (floats_to_e4m3x2((v[2] - f23.x) * 32.0f, (v[3] - f23.y) * 32.0f) << 16);
+          }
+          if constexpr (S::kQShared) {
+            shared[(ks * NT + n) * 32 + lane] = make_uint4(code[0], code[1], code[2], code[3]);
           } else {
-            a[r] = __ldg(reinterpret_cast<const uint32_t*>(row) + t);
-            a[2 + r] = __ldg(reinterpret_cast<const uint32_t*>(row) + t + 4);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) q[n][ks][i] = code[i];
           }
         }
       }
-      if constexpr (S::kQShared) {
-        shared[ks * 32 + lane] = make_uint4(a[0], a[1], a[2], a[3]);
+    }
+  }
+
+  __device__ __forceinline__ void fragment(uint32_t (&b)[kQWords], int n, int ks, const uint4* shared) const {
+    if constexpr (S::kQShared) {
+      const int at = (ks * NT + n) * 32 + (threadIdx.x & 31);
+      if constexpr (kE4m3) {
+        const uint4 w = shared[at];
+        b[0] = w.x;
+        b[1] = w.y;
+        b[kQWords - 2] = w.z;
+        b[kQWords - 1] = w.w;
       } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) q[ks][i] = a[i];
+        const uint2 w = reinterpret_cast<const uint2*>(shared)[at];
+        b[0] = w.x;
+        b[1] = w.y;
       }
+    } else {
+#pragma unroll
+      for (int i = 0; i < kQWords; ++i) b[i] = q[n][ks][i];
     }
   }
 
@@ -265,193 +339,218 @@ struct AttendWarp {
   }
 
   // One tile: scores, softmax, and the products with V.
-  __device__ __forceinline__ void tile(const AttendArgs& p, uint32_t kt, uint32_t vt, const float* scales, uint32_t valid,
+  __device__ __forceinline__ void tile(uint32_t kt, uint32_t vt, const float* scales, uint32_t valid,
                                        const uint4* shared_q) {
-    const int lane = threadIdx.x & 31, t = lane & 3;
+    const int lane = threadIdx.x & 31, g = lane >> 2;
     const float ninf = __int_as_float(0xff800000);
-    float s[kTiles][4];
+    float s[NT][kGroups][4], low[NT][kE4m3 ? kGroups : 1][4];
 #pragma unroll
-    for (int n = 0; n < kTiles; ++n)
+    for (int n = 0; n < NT; ++n)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) s[n][i] = 0.0f;
-    constexpr int kStepsPerLoad = kE4m3 ? 4 : 2;
+      for (int k = 0; k < kGroups; ++k)
 #pragma unroll
-    for (int j = 0; j < S::kChunks / 4; ++j) {
-      uint32_t a[kStepsPerLoad][4];
-#pragma unroll
-      for (int i = 0; i < kStepsPerLoad; ++i) {
-        if constexpr (S::kQShared) {
-          const uint4 w = shared_q[(j * kStepsPerLoad + i) * 32 + lane];
-          a[i][0] = w.x;
-          a[i][1] = w.y;
-          a[i][2] = w.z;
-          a[i][3] = w.w;
-        } else {
-#pragma unroll
-          for (int x = 0; x < 4; ++x) a[i][x] = q[j * kStepsPerLoad + i][x];
+        for (int i = 0; i < 4; ++i) {
+          s[n][k][i] = 0.0f;
+          if constexpr (kE4m3) low[n][k][i] = 0.0f;
         }
-      }
 #pragma unroll
-      for (int n = 0; n < kTiles; ++n) {
-        uint32_t b[4];
-        load_matrices(b, chunk_at(kt, n * 8 + (lane & 7), j * 4 + (lane >> 3)));
-        if constexpr (kE4m3) {
+    for (int ks = 0; ks < kSteps; ++ks) {
+      uint32_t b[NT][kQWords];
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            mma16816<true>(s[n], a[i], e4m3x2_to_f16x2(b[i] & 0xffffu), e4m3x2_to_f16x2(b[i] >> 16));
-        } else {
-          mma16816<false>(s[n], a[0], b[0], b[1]);
-          mma16816<false>(s[n], a[1], b[2], b[3]);
+      for (int n = 0; n < NT; ++n) fragment(b[n], n, ks, shared_q);
+#pragma unroll
+      for (int k = 0; k < kGroups; ++k) {
+        uint32_t a[4];
+        load_matrices(a, chunk_at(kt, k * 16 + (lane & 15), 2 * ks + (lane >> 4)));
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          if constexpr (kE4m3) {
+            mma16832_e4m3(s[n][k], a, b[n][0], b[n][1]);
+            mma16832_e4m3(low[n][k], a, b[n][kQWords - 2], b[n][kQWords - 1]);
+          } else {
+            mma16816<false>(s[n][k], a, b[n][0], b[n][1]);
+          }
         }
       }
     }
     // scores in log2 units; keys left out become -inf
-    float top[2] = {ninf, ninf};
 #pragma unroll
-    for (int n = 0; n < kTiles; ++n) {
-      float2 ks = make_float2(1.0f, 1.0f);
-      if constexpr (kE4m3) ks = *reinterpret_cast<const float2*>(scales + n * 8 + 2 * t);
+    for (int k = 0; k < kGroups; ++k)
 #pragma unroll
-      for (int r = 0; r < kRows; ++r) {
-        if constexpr (kE4m3) {
-          s[n][2 * r] *= ks.x;
-          s[n][2 * r + 1] *= ks.y;
-        }
-        s[n][2 * r] *= row_scale[r];
-        s[n][2 * r + 1] *= row_scale[r];
+      for (int y = 0; y < 2; ++y) {  // key k * 16 + g + 8 y
+        float ks = 1.0f;
+        if constexpr (kE4m3) ks = scales[k * 16 + g + 8 * y];
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            float& x = s[n][k][2 * y + h];
+            if constexpr (kE4m3)
+              x = fmaf(low[n][k][2 * y + h], 0.03125f, x) * ks * head_scale[n][h];
+            else
+              x *= head_scale[n][h];
+          }
       }
-    }
     if (valid != (S::kKeys == 32 ? 0xffffffffu : (1u << (S::kKeys & 31)) - 1u)) {
 #pragma unroll
-      for (int n = 0; n < kTiles; ++n)
+      for (int k = 0; k < kGroups; ++k)
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
-          if (!((valid >> (n * 8 + 2 * t + i)) & 1u)) s[n][i] = s[n][2 + i] = ninf;
+        for (int y = 0; y < 2; ++y)
+          if (!((valid >> (k * 16 + g + 8 * y)) & 1u))
+#pragma unroll
+            for (int n = 0; n < NT; ++n) s[n][k][2 * y] = s[n][k][2 * y + 1] = ninf;
     }
-#pragma unroll
-    for (int n = 0; n < kTiles; ++n)
-#pragma unroll
-      for (int r = 0; r < kRows; ++r) top[r] = fmaxf(top[r], fmaxf(s[n][2 * r], s[n][2 * r + 1]));
-#pragma unroll
-    for (int r = 0; r < kRows; ++r) top[r] = quad_max(top[r]);
     // The reference m moves only when a score passes it by 2^8: weights up to
-    // 256 are harmless in fp32 sums, and most tiles need no rescaling.
-    bool raise = top[0] > m[0] + 8.0f;
-    if constexpr (kFull) raise |= top[1] > m[1] + 8.0f;
+    // 256 are harmless in fp32 sums, and most tiles need neither a maximum
+    // across lanes nor a rescaling.
+    float top[NT][2];
+    bool raise = false;
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        top[n][h] = ninf;
+#pragma unroll
+        for (int k = 0; k < kGroups; ++k) top[n][h] = fmaxf(top[n][h], fmaxf(s[n][k][h], s[n][k][2 + h]));
+        raise |= top[n][h] > m[n][h] + 8.0f;
+      }
     if (__any_sync(0xffffffffu, raise)) {
 #pragma unroll
-      for (int r = 0; r < kRows; ++r) {
-        const float mn = fmaxf(m[r], top[r]);
-        const float x = exp2_fast(m[r] - finite_or_zero(mn));
-        m[r] = mn;
-        l[r] *= x;
-        if constexpr (kE4m3) {
-          f[r] *= x;
-        } else {
+      for (int n = 0; n < NT; ++n)
 #pragma unroll
-          for (int j = 0; j < D / 8; ++j) {
-            o[j][2 * r] *= x;
-            o[j][2 * r + 1] *= x;
+        for (int h = 0; h < 2; ++h) {
+          const float mn = fmaxf(m[n][h], column_max(top[n][h]));
+          const float x = exp2_fast(m[n][h] - finite_or_zero(mn));
+          m[n][h] = mn;
+          l[n][h] *= x;
+          if constexpr (kE4m3) {
+            f[n][h] *= x;
+          } else {
+#pragma unroll
+            for (int j = 0; j < D / 16; ++j) {
+              o[n][j][h] *= x;
+              o[n][j][2 + h] *= x;
+            }
           }
         }
-      }
     }
 #pragma unroll
-    for (int r = 0; r < kRows; ++r) {
-      const float ref = finite_or_zero(m[r]);
+    for (int n = 0; n < NT; ++n)
 #pragma unroll
-      for (int n = 0; n < kTiles; ++n) {
-        s[n][2 * r] = exp2_fast(s[n][2 * r] - ref);
-        s[n][2 * r + 1] = exp2_fast(s[n][2 * r + 1] - ref);
-        l[r] += s[n][2 * r] + s[n][2 * r + 1];
+      for (int h = 0; h < 2; ++h) {
+        const float ref = finite_or_zero(m[n][h]);
+#pragma unroll
+        for (int k = 0; k < kGroups; ++k) {
+          s[n][k][h] = exp2_fast(s[n][k][h] - ref);
+          s[n][k][2 + h] = exp2_fast(s[n][k][2 + h] - ref);
+          l[n][h] += s[n][k][h] + s[n][k][2 + h];
+        }
       }
-    }
     if constexpr (kE4m3) {
       // w_j = p_j * vscale_j, held in f16 relative to f: f follows the largest
-      // w of the row, so the weights that carry the sum keep 11 bits whatever
+      // w of the head, so the weights that carry the sum keep 11 bits whatever
       // the scales are.
-      float wt[2] = {0.0f, 0.0f};
+      float wt[NT][2];
 #pragma unroll
-      for (int n = 0; n < kTiles; ++n) {
-        const float2 vs = *reinterpret_cast<const float2*>(scales + S::kKeys + n * 8 + 2 * t);
+      for (int n = 0; n < NT; ++n) wt[n][0] = wt[n][1] = 0.0f;
 #pragma unroll
-        for (int r = 0; r < kRows; ++r) {
-          s[n][2 * r] *= vs.x;
-          s[n][2 * r + 1] *= vs.y;
-          wt[r] = fmaxf(wt[r], fmaxf(fabsf(s[n][2 * r]), fabsf(s[n][2 * r + 1])));
+      for (int k = 0; k < kGroups; ++k)
+#pragma unroll
+        for (int y = 0; y < 2; ++y) {
+          const float vs = scales[S::kKeys + k * 16 + g + 8 * y];
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              s[n][k][2 * y + h] *= vs;
+              wt[n][h] = fmaxf(wt[n][h], fabsf(s[n][k][2 * y + h]));
+            }
         }
-      }
+      bool grow = false;
 #pragma unroll
-      for (int r = 0; r < kRows; ++r) wt[r] = fminf(quad_max(wt[r]), 1e36f);
-      bool grow = wt[0] > f[0] * 256.0f;
-      if constexpr (kFull) grow |= wt[1] > f[1] * 256.0f;
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) grow |= wt[n][h] > f[n][h] * 256.0f;
       if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
-        for (int r = 0; r < kRows; ++r) {
-          const float fn = fmaxf(f[r], wt[r]);
-          const float x = fn > 0.0f ? f[r] / fn : 0.0f;
-          f[r] = fn;
+        for (int n = 0; n < NT; ++n)
 #pragma unroll
-          for (int j = 0; j < D / 8; ++j) {
-            o[j][2 * r] *= x;
-            o[j][2 * r + 1] *= x;
+          for (int h = 0; h < 2; ++h) {
+            const float fn = fmaxf(f[n][h], fminf(column_max(wt[n][h]), 1e36f));
+            const float x = fn > 0.0f ? f[n][h] / fn : 0.0f;
+            f[n][h] = fn;
+#pragma unroll
+            for (int j = 0; j < D / 16; ++j) {
+              o[n][j][h] *= x;
+              o[n][j][2 + h] *= x;
+            }
+          }
+      }
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const float inv = f[n][h] >= 1.2e-38f ? 1.0f / f[n][h] : 0.0f;  // weights below 2^-126 count as nothing
+#pragma unroll
+          for (int k = 0; k < kGroups; ++k) {
+            s[n][k][h] *= inv;
+            s[n][k][2 + h] *= inv;
           }
         }
-      }
-#pragma unroll
-      for (int r = 0; r < kRows; ++r) {
-        const float inv = f[r] >= 1.2e-38f ? 1.0f / f[r] : 0.0f;  // weights below 2^-126 count as nothing
-#pragma unroll
-        for (int n = 0; n < kTiles; ++n) {
-          s[n][2 * r] *= inv;
-          s[n][2 * r + 1] *= inv;
-        }
-      }
     }
 #pragma unroll
-    for (int kk = 0; kk < S::kKeys / 16; ++kk) {
-      // P as the left operand: its C layout is the A layout of 16 keys.  Beside
-      // bf16 values P is split into two bf16 parts (the second takes what
-      // rounding the first left), which keeps 16 bits of every weight.
-      uint32_t hi[4] = {0, 0, 0, 0}, lo[4] = {0, 0, 0, 0};
+    for (int k = 0; k < kGroups; ++k) {
+      // P^T as the right operand.  Beside bf16 values P is split into two bf16
+      // parts (the second takes what rounding the first left), which keeps 16
+      // bits of every weight.
+      uint32_t hi[NT][2], lo[NT][2];
 #pragma unroll
-      for (int x = 0; x < 2; ++x)
+      for (int n = 0; n < NT; ++n)
 #pragma unroll
-        for (int r = 0; r < kRows; ++r) {
-          const float a = s[2 * kk + x][2 * r], b = s[2 * kk + x][2 * r + 1];
+        for (int y = 0; y < 2; ++y) {
+          const float a = s[n][k][2 * y], b = s[n][k][2 * y + 1];
           if constexpr (kE4m3) {
-            hi[2 * x + r] = floats_to_f16x2(a, b);
+            hi[n][y] = transpose8x8(floats_to_f16x2(a, b));
           } else {
             const uint32_t h = floats_to_bf16x2(a, b);
-            hi[2 * x + r] = h;
-            lo[2 * x + r] = floats_to_bf16x2(a - __uint_as_float(h << 16), b - __uint_as_float(h & 0xffff0000u));
+            hi[n][y] = transpose8x8(h);
+            lo[n][y] = transpose8x8(
+                floats_to_bf16x2(a - __uint_as_float(h << 16), b - __uint_as_float(h & 0xffff0000u)));
           }
         }
+      if constexpr (kE4m3) {
 #pragma unroll
-      for (int c = 0; c < S::kChunks; c += 2) {
-        uint32_t b[4];
-        load_matrices_t(b, chunk_at(vt, kk * 16 + (lane & 15), c + (lane >> 4)));
-        if constexpr (kE4m3) {
+        for (int c = 0; c < S::kChunks; c += 2) {
+          uint32_t r[4];
+          load_matrices_t(r, chunk_at(vt, k * 16 + (lane & 15), c + (lane >> 4)));
 #pragma unroll
-          for (int x = 0; x < 2; ++x) {  // chunk c + x: even columns, then odd ones
-            mma16816<true>(o[2 * (c + x)], hi, e4m3x2_to_f16x2(__byte_perm(b[2 * x], 0, 0x4420)),
-                           e4m3x2_to_f16x2(__byte_perm(b[2 * x + 1], 0, 0x4420)));
-            mma16816<true>(o[2 * (c + x) + 1], hi, e4m3x2_to_f16x2(__byte_perm(b[2 * x], 0, 0x4431)),
-                           e4m3x2_to_f16x2(__byte_perm(b[2 * x + 1], 0, 0x4431)));
+          for (int x = 0; x < 2; ++x) {  // chunk c + x: its even columns as rows 0-7, its odd ones as rows 8-15
+            const uint32_t a[4] = {
+                e4m3x2_to_f16x2(__byte_perm(r[2 * x], 0, 0x4420)), e4m3x2_to_f16x2(__byte_perm(r[2 * x], 0, 0x4431)),
+                e4m3x2_to_f16x2(__byte_perm(r[2 * x + 1], 0, 0x4420)),
+                e4m3x2_to_f16x2(__byte_perm(r[2 * x + 1], 0, 0x4431))};
+#pragma unroll
+            for (int n = 0; n < NT; ++n) mma16816<true>(o[n][c + x], a, hi[n][0], hi[n][1]);
           }
-        } else {
-          mma16816<false>(o[c], hi, b[0], b[1]);
-          mma16816<false>(o[c + 1], hi, b[2], b[3]);
-          mma16816<false>(o[c], lo, b[0], b[1]);
-          mma16816<false>(o[c + 1], lo, b[2], b[3]);
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < D / 16; ++j) {
+          uint32_t a[4];
+          load_matrices_t(a, chunk_at(vt, k * 16 + (lane & 7) + (lane >> 4) * 8, 2 * j + ((lane >> 3) & 1)));
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            mma16816<false>(o[n][j], a, hi[n][0], hi[n][1]);
+            mma16816<false>(o[n][j], a, lo[n][0], lo[n][1]);
+          }
         }
       }
     }
   }
 
-  // Column of o[j][i] (i = 0, 1) for a lane with lane % 4 = t.
-  static __device__ __forceinline__ int column(int j, int i, int t) {
-    return kE4m3 ? (j >> 1) * 16 + 4 * t + 2 * i + (j & 1) : 8 * j + 2 * t + i;
+  // Column of o[.][j][i] for a lane with lane / 4 = g.
+  static __device__ __forceinline__ int column(int j, int i, int g) {
+    return kE4m3 ? 16 * j + 2 * g + (i >> 1) : 16 * j + g + 8 * (i >> 1);
   }
 };
 
@@ -534,11 +633,11 @@ __device__ void attend_join(const AttendArgs& p, int first, int last, int rows, 
 }
 
 // ---------------------------------------------------------------- kernel
-template <int D, bool kE4m3, bool kFull>
-__global__ void __launch_bounds__(kAttendThreads, AttendShape<D, kE4m3>::kCtasPerSm)
+template <int D, bool kE4m3, int NT>
+__global__ void __launch_bounds__(kAttendThreads, (AttendShape<D, kE4m3, NT>::kCtasPerSm))
     paged_attention_kernel(AttendArgs p) {
-  using S = AttendShape<D, kE4m3>;
-  using W = AttendWarp<D, kE4m3, kFull>;
+  using S = AttendShape<D, kE4m3, NT>;
+  using W = AttendWarp<D, kE4m3, NT>;
   extern __shared__ __align__(128) unsigned char smem[];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   float* join = reinterpret_cast<float*>(smem + S::kOffJoin);
@@ -575,7 +674,7 @@ __global__ void __launch_bounds__(kAttendThreads, AttendShape<D, kE4m3>::kCtasPe
   };
   if (p.positions) {
     cur.b = 0;
-    cursor_enter<D, kE4m3>(p, cur);
+    cursor_enter<S::kGranule>(p, cur);
     total = static_cast<int64_t>(p.tab.batch) * units * cur.granules;
     share();
     const int64_t u = g0 / cur.granules;
@@ -617,7 +716,7 @@ __global__ void __launch_bounds__(kAttendThreads, AttendShape<D, kE4m3>::kCtasPe
     __syncthreads();
     if (g0 < g1) {
       cur.b = static_cast<int>(plan[4]);
-      cursor_enter<D, kE4m3>(p, cur);
+      cursor_enter<S::kGranule>(p, cur);
       cur.unit = static_cast<int>(plan[5] / cur.granules);
       cur.at = static_cast<int>(plan[5] - static_cast<int64_t>(cur.unit) * cur.granules);
     }
@@ -643,7 +742,7 @@ __global__ void __launch_bounds__(kAttendThreads, AttendShape<D, kE4m3>::kCtasPe
       if (lane < S::kKeys && i < static_cast<uint32_t>(ahead.count))
         tok = p.positions ? __ldg(p.positions + (static_cast<int64_t>(ahead.b) * p.lists + list) * p.c + i) : static_cast<int>(i);
       --ahead_left;
-      cursor_next<D, kE4m3>(p, ahead);
+      cursor_next<S::kGranule>(p, ahead);
     }
   };
   auto next_page = [&]() {
@@ -651,7 +750,7 @@ __global__ void __launch_bounds__(kAttendThreads, AttendShape<D, kE4m3>::kCtasPe
     page_kv = tok_kv;
     if (tok >= 0) {
       if (tok < tok_len) {
-        const int at = tok / p.k.page_size;
+        const int at = static_cast<int>((static_cast<uint64_t>(tok) * p.page_magic) >> p.page_shift);
         off = tok - at * p.k.page_size;
         page = __ldg(p.tab.table + tok_b * p.tab.stride + at);
         if (page < 0 || page >= p.k.pages) {
@@ -675,15 +774,30 @@ __global__ void __launch_bounds__(kAttendThreads, AttendShape<D, kE4m3>::kCtasPe
     if (lane == 0) valid_masks[stage] = valid;
     if (valid) {
       constexpr int kRowsPerCopy = 32 / S::kChunks;
-      const int c = lane % S::kChunks;
+      const int c = lane % S::kChunks, r0 = lane / S::kChunks;
+      if (p.grouped && p.same_strides) {  // one address for 16 rows of K and of V
 #pragma unroll
-      for (int i = 0; i < S::kKeys / kRowsPerCopy; ++i) {
-        const int r = i * kRowsPerCopy + lane / S::kChunks;
-        const int64_t a = __shfl_sync(0xffffffffu, ko, r);
-        const bool on = (valid >> r) & 1u;
-        copy16(W::chunk_at(kt, r, c), p.k.data + a + c * 16, on);
-        const int64_t b = p.same_strides ? a : __shfl_sync(0xffffffffu, vo, r);
-        copy16(W::chunk_at(vt, r, c), p.v.data + b + c * 16, on);
+        for (int y = 0; y < S::kKeys / 16; ++y) {
+          int64_t a = __shfl_sync(0xffffffffu, ko, y * 16) + r0 * p.k.token_stride + c * 16;
+#pragma unroll
+          for (int i = 0; i < 16 / kRowsPerCopy; ++i) {
+            const int r = y * 16 + i * kRowsPerCopy + r0;
+            const bool on = (valid >> r) & 1u;
+            copy16(W::chunk_at(kt, r, c), p.k.data + a, on);
+            copy16(W::chunk_at(vt, r, c), p.v.data + a, on);
+            a += kRowsPerCopy * p.k.token_stride;
+          }
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < S::kKeys / kRowsPerCopy; ++i) {
+          const int r = i * kRowsPerCopy + r0;
+          const int64_t a = __shfl_sync(0xffffffffu, ko, r) + c * 16;
+          const bool on = (valid >> r) & 1u;
+          copy16(W::chunk_at(kt, r, c), p.k.data + a, on);
+          const int64_t b = p.same_strides ? a : __shfl_sync(0xffffffffu, vo, r) + c * 16;
+          copy16(W::chunk_at(vt, r, c), p.v.data + b, on);
+        }
       }
       if constexpr (kE4m3) {
         if (lane < S::kKeys) {
@@ -733,7 +847,7 @@ __global__ void __launch_bounds__(kAttendThreads, AttendShape<D, kE4m3>::kCtasPe
     const uint32_t valid = valid_masks[stage];
     if (valid) {
       const uint32_t kt = ring_addr + stage * S::kStageBytes;
-      w.tile(p, kt, kt + S::kTileBytes,
+      w.tile(kt, kt + S::kTileBytes,
              reinterpret_cast<const float*>(ring + stage * S::kStageBytes + 2 * S::kTileBytes), valid, shared_q);
     }
     stage = stage == S::kStages - 1 ? 0 : stage + 1;
@@ -745,27 +859,29 @@ __global__ void __launch_bounds__(kAttendThreads, AttendShape<D, kE4m3>::kCtasPe
     // The unit ends here, or this CTA's share of it: join the four warps.
     const int64_t unit_first = g - cur.at;
     const bool whole = unit_first >= g0 && cur.at + 1 == cur.granules;
-    const int t = lane & 3, row = lane >> 2;
+    const int t = lane & 3, lane_g = lane >> 2;
 #pragma unroll
-    for (int r = 0; r < W::kRows; ++r) {
-      float s = w.l[r];
-      s += __shfl_xor_sync(0xffffffffu, s, 1);
-      s += __shfl_xor_sync(0xffffffffu, s, 2);
-      if (t == 0) {
-        ml[warp * 32 + row + 8 * r] = w.m[r];
-        ml[warp * 32 + 16 + row + 8 * r] = s;
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const float sum = column_sum(w.l[n][h]);
+        if (lane_g == 0) {
+          ml[warp * 32 + n * 8 + 2 * t + h] = w.m[n][h];
+          ml[warp * 32 + 16 + n * 8 + 2 * t + h] = sum;
+        }
       }
-    }
     __syncthreads();
-    float factor[2] = {0.0f, 0.0f};
+    float factor[NT][2];
 #pragma unroll
-    for (int r = 0; r < W::kRows; ++r) {
-      float mm = w.m[r];
+    for (int n = 0; n < NT; ++n)
 #pragma unroll
-      for (int x = 0; x < kAttendWarps; ++x) mm = fmaxf(mm, ml[x * 32 + row + 8 * r]);
-      factor[r] = exp2_fast(w.m[r] - finite_or_zero(mm));
-      if constexpr (kE4m3) factor[r] *= w.f[r];
-    }
+      for (int h = 0; h < 2; ++h) {
+        float mm = w.m[n][h];
+#pragma unroll
+        for (int x = 0; x < kAttendWarps; ++x) mm = fmaxf(mm, ml[x * 32 + n * 8 + 2 * t + h]);
+        factor[n][h] = exp2_fast(w.m[n][h] - finite_or_zero(mm));
+        if constexpr (kE4m3) factor[n][h] *= w.f[n][h];
+      }
     float* part = p.parts + static_cast<int64_t>(blockIdx.x * 2 + (unit_first >= g0)) * attend_part_floats(D);
     const int64_t out_row = static_cast<int64_t>(cur.b) * p.heads + head;
     float* inverse = ml + kAttendWarps * 32;  // 1 / l of every row, for rows that end here
@@ -783,34 +899,38 @@ __global__ void __launch_bounds__(kAttendThreads, AttendShape<D, kE4m3>::kCtasPe
         p.lse[out_row + tid] = 0.6931471805599453f * (mm + log2f(sum));
       }
     }
+    const int columns = S::join_columns(rows), pitch = columns + 4;
+    for (int c0 = 0; c0 < D; c0 += columns) {
+      if (c0) __syncthreads();
 #pragma unroll
-    for (int c0 = 0; c0 < D; c0 += S::kJoinCols) {
-#pragma unroll 1
-      for (int x = 0; x < kAttendWarps; ++x) {  // in warp order
-        if (warp == x) {
+      for (int j = 0; j < D / 16; ++j) {
+        if (j * 16 < c0 || j * 16 >= c0 + columns) continue;
 #pragma unroll
-          for (int j = c0 / 8; j < (c0 + S::kJoinCols) / 8; ++j)
+        for (int n = 0; n < NT; ++n)
 #pragma unroll
-            for (int r = 0; r < W::kRows; ++r)
-#pragma unroll
-              for (int i = 0; i < 2; ++i) {
-                float* dst = join + (row + 8 * r) * S::kJoinPitch + W::column(j, i, t) - c0;
-                const float v = w.o[j][2 * r + i] * factor[r];
-                *dst = x == 0 ? v : *dst + v;
-              }
-        }
-        __syncthreads();
+          for (int i = 0; i < 4; ++i) {
+            const int head_row = n * 8 + 2 * t + (i & 1);
+            if (head_row < rows)
+              join[(warp * rows + head_row) * pitch + W::column(j, i, lane_g) - c0] = w.o[n][j][i] * factor[n][i & 1];
+          }
       }
-      for (int i = tid; i < rows * (S::kJoinCols / 2); i += kAttendThreads) {
-        const int y = i / (S::kJoinCols / 2), c = i % (S::kJoinCols / 2) * 2;
-        const float2 v = *reinterpret_cast<const float2*>(join + y * S::kJoinPitch + c);
+      __syncthreads();
+      const int pairs = min(columns, D - c0) / 2;
+      for (int i = tid; i < rows * pairs; i += kAttendThreads) {
+        const int y = i / pairs, c = (i - y * pairs) * 2;
+        float2 v = make_float2(0.0f, 0.0f);
+#pragma unroll
+        for (int x = 0; x < kAttendWarps; ++x) {  // in warp order
+          const float2 u = *reinterpret_cast<const float2*>(join + (x * rows + y) * pitch + c);
+          v.x += u.x;
+          v.y += u.y;
+        }
         if (whole)
           *reinterpret_cast<uint32_t*>(p.out + (out_row + y) * D + c0 + c) =
               floats_to_bf16x2(v.x * inverse[y], v.y * inverse[y]);
         else
           *reinterpret_cast<float2*>(part + 32 + y * D + c0 + c) = v;
       }
-      if (c0 + S::kJoinCols < D) __syncthreads();
     }
     if (!whole) {
       const int first = part_of(unit_first, total, ctas, 1);
@@ -832,7 +952,7 @@ __global__ void __launch_bounds__(kAttendThreads, AttendShape<D, kE4m3>::kCtasPe
     __syncthreads();
     w.reset();
     fresh = true;
-    cursor_next<D, kE4m3>(p, cur);
+    cursor_next<S::kGranule>(p, cur);
   }
   copy_wait<0>();
 }

@@ -328,9 +328,11 @@ int cache_read(const topk_cache *cache, const int32_t *block_table_dev, int64_t 
  * A head with no token to attend to, or whose scores are all -inf, gives
  * zeros and an lse of -inf.
  * The workspace holds paged_attention_workspace_bytes(...) bytes, 16-byte
- * aligned, zero-filled before its first use; a call leaves it ready for any
+ * aligned.  Its first TOPK_DECODE_TICKET_BYTES must be zero before its first
+ * use and are zero again after every call; the rest is scratch.  It serves any
  * later call of this operator or of topk_beam (not of the selections above),
  * and calls that overlap on the GPU must not share one. */
+#define TOPK_DECODE_TICKET_BYTES 16384
 int paged_attention(const uint16_t *q_dev, int64_t q_stride, int64_t batch, int heads,
                     const topk_cache *k_cache, const topk_cache *v_cache,
                     const int32_t *block_table_dev, int64_t table_stride, int table_width,
