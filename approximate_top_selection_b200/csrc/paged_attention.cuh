@@ -124,12 +124,13 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-__device__ __forceinline__ void mma16832_e4m3(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-      "{%0, %1, %2, %3};"
-      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+// Two 16x16 matrices of bytes, transposed: r[2 x] holds rows 4t .. 4t + 3 of
+// column g of matrix x, r[2 x + 1] the same of column g + 8.
+__device__ __forceinline__ void load_bytes_t(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m16n16.x2.trans.shared.b8 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
 }
 // Transposes an 8x8 matrix of 16-bit values held across the warp.
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
@@ -198,15 +199,18 @@ __device__ __forceinline__ void cursor_next(const AttendArgs& p, AttendCursor& u
 }
 
 // ---------------------------------------------------------------- one warp's state
-// A lane's place in the products: g = lane / 4, t = lane % 4.  Scores: keys g
-// and g + 8 of each 16, heads 2t and 2t + 1 of each 8.  O^T: columns of V by g,
-// the same heads.
+// A lane's place in the products: g = lane / 4, t = lane % 4.  Scores: rows g
+// and g + 8 of each 16, heads 2t and 2t + 1 of each 8; O^T: columns g and g + 8
+// of each 16 of V, the same heads.  Row r of a score tile is key_of(r): the
+// order of summation over keys is free, and bytes of V come transposed four
+// keys at a time, so that with the keys 4t, 4t + 1 in rows 2t, 2t + 1 and 4t + 2,
+// 4t + 3 in rows 2t + 8, 2t + 9 each half of such a word is an operand pair.
 template <int D, bool kE4m3, int NT>
 struct AttendWarp {
   using S = AttendShape<D, kE4m3, NT>;
   static constexpr int kGroups = S::kKeys / 16;
-  static constexpr int kSteps = kE4m3 ? D / 32 : D / 16;  // of the product over d
-  static constexpr int kQWords = kE4m3 ? 4 : 2;           // registers of Q per step and 8 heads
+  static constexpr int kSteps = D / 16;  // of the product over d
+  static constexpr int kQWords = 2;      // registers of Q per step and 8 heads
 
   float o[NT][D / 16][4];
   float m[NT][2], l[NT][2];
@@ -230,37 +234,28 @@ struct AttendWarp {
     }
   }
 
+  static __device__ __forceinline__ int key_of(int r) {
+    return kE4m3 ? ((r & 6) << 1) + (r & 1) + ((r >> 2) & 2) : r;
+  }
+
   // Fragments of the query heads (zeros behind `rows`).  Beside e4m3 keys the
-  // product runs in e4m3 too, on the codes as they lie in the cache: a head is
-  // scaled by the power of two that brings its largest finite value into
-  // [128, 256) and split into two codes, q = a + b / 32.  a keeps 4 significant
-  // bits and b the next 4, all a bf16 value has; what is below 2^-14 of the
-  // head's largest value keeps an absolute error of 2^-22 of that value, as
-  // much as the fp32 sum itself.  (An infinity in q counts as NaN there.)
-  __device__ __forceinline__ void load_q(const AttendArgs& p, const uint16_t* q0, int rows, uint4* shared, int warp) {
+  // products run in f16, which holds every code exactly: a head is scaled by
+  // the power of two that brings its largest finite value into [2^14, 2^15),
+  // where rounding to f16 moves a value by at most 2^-25 (below 2^-39 of that
+  // largest one).  A lane's four codes of a key are the values 4t .. 4t + 3 of
+  // 16, and so are its values of q.
+  __device__ __forceinline__ void load_q(const AttendArgs& p, const uint16_t* q0, int rows, uint2* shared, int warp) {
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
       const bool live = n * 8 + g < rows;
       const uint16_t* row = q0 + static_cast<int64_t>(n * 8 + g) * D;
+      float mul = 1.0f;
       head_scale[n][0] = head_scale[n][1] = p.scale_log2;
-      if constexpr (!kE4m3) {
-#pragma unroll
-        for (int ks = 0; ks < kSteps; ++ks) {
-          if (S::kQShared && ks % kAttendWarps != warp) continue;
-          const uint32_t* src = reinterpret_cast<const uint32_t*>(row + ks * 16);
-          const uint32_t b0 = live ? __ldg(src + t) : 0u, b1 = live ? __ldg(src + t + 4) : 0u;
-          if constexpr (S::kQShared) {
-            reinterpret_cast<uint2*>(shared)[(ks * NT + n) * 32 + lane] = make_uint2(b0, b1);
-          } else {
-            q[n][ks][0] = b0;
-            q[n][ks][1] = b1;
-          }
-        }
-      } else {
+      if constexpr (kE4m3) {
         uint32_t top = 0;
 #pragma unroll 4
-        for (int ks = 0; ks < D / 16; ++ks) {
+        for (int ks = 0; ks < kSteps; ++ks) {
           const uint2 w = live ? __ldg(reinterpret_cast<const uint2*>(row + ks * 16) + t) : make_uint2(0, 0);
           const uint32_t h[4] = {w.x << 16, w.x, w.y << 16, w.y};
 #pragma unroll
@@ -271,104 +266,96 @@ struct AttendWarp {
         }
         top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
         top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-        float mul = 1.0f, scale = p.scale_log2;
+        float scale = p.scale_log2;
         if (top) {
-          int e = 7 - (static_cast<int>(top >> 23) - 127);
+          int e = 14 - (static_cast<int>(top >> 23) - 127);
           e = min(max(e, -126), 126);
           mul = power_of_two(e);
           scale = p.scale_log2 * power_of_two(-e);
         }
         head_scale[n][0] = __shfl_sync(0xffffffffu, scale, 8 * t);
         head_scale[n][1] = __shfl_sync(0xffffffffu, scale, 8 * t + 4);
+      }
 #pragma unroll
-        for (int ks = 0; ks < kSteps; ++ks) {
-          if (S::kQShared && ks % kAttendWarps != warp) continue;
-          uint32_t code[4];
-#pragma unroll
-          for (int half = 0; half < 2; ++half) {  // 16 values each, four of them this lane's
-            const uint2 w = live ? __ldg(reinterpret_cast<const uint2*>(row + ks * 32 + half * 16) + t) : make_uint2(0, 0);
-            float v[4] = {__uint_as_float(w.x << 16) * mul, __uint_as_float(w.x & 0xffff0000u) * mul,
-                          __uint_as_float(w.y << 16) * mul, __uint_as_float(w.y & 0xffff0000u) * mul};
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              if (!(fabsf(v[i]) < __int_as_float(0x7f800000))) v[i] = __int_as_float(0x7fffffff);
-            const uint32_t a01 = floats_to_e4m3x2(v[0], v[1]), a23 = floats_to_e4m3x2(v[2], v[3]);
-            const float2 f01 = f16x2_to_float2(e4m3x2_to_f16x2(a01)), f23 = f16x2_to_float2(e4m3x2_to_f16x2(a23));
-            code[half] = a01 | (a23 << 16);
-            code[2 + half] = floats_to_e4m3x2((v[0] - f01.x) * 32.0f, (v[1] - f01.y) * 32.0f) |
-                             (floats_to_e4m3x2((v[2] - f23.x) * 32.0f, (v[3] - f23.y) * 32.0f) << 16);
-          }
-          if constexpr (S::kQShared) {
-            shared[(ks * NT + n) * 32 + lane] = make_uint4(code[0], code[1], code[2], code[3]);
+      for (int ks = 0; ks < kSteps; ++ks) {
+        if (S::kQShared && ks % kAttendWarps != warp) continue;
+        uint32_t b0 = 0, b1 = 0;
+        if (live) {
+          if constexpr (kE4m3) {
+            const uint2 w = __ldg(reinterpret_cast<const uint2*>(row + ks * 16) + t);
+            b0 = floats_to_f16x2(__uint_as_float(w.x << 16) * mul, __uint_as_float(w.x & 0xffff0000u) * mul);
+            b1 = floats_to_f16x2(__uint_as_float(w.y << 16) * mul, __uint_as_float(w.y & 0xffff0000u) * mul);
           } else {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) q[n][ks][i] = code[i];
+            const uint32_t* src = reinterpret_cast<const uint32_t*>(row + ks * 16);
+            b0 = __ldg(src + t);
+            b1 = __ldg(src + t + 4);
           }
+        }
+        if constexpr (S::kQShared) {
+          shared[(ks * NT + n) * 32 + lane] = make_uint2(b0, b1);
+        } else {
+          q[n][ks][0] = b0;
+          q[n][ks][1] = b1;
         }
       }
     }
   }
 
-  __device__ __forceinline__ void fragment(uint32_t (&b)[kQWords], int n, int ks, const uint4* shared) const {
+  __device__ __forceinline__ void fragment(uint32_t (&b)[kQWords], int n, int ks, const uint2* shared) const {
     if constexpr (S::kQShared) {
-      const int at = (ks * NT + n) * 32 + (threadIdx.x & 31);
-      if constexpr (kE4m3) {
-        const uint4 w = shared[at];
-        b[0] = w.x;
-        b[1] = w.y;
-        b[kQWords - 2] = w.z;
-        b[kQWords - 1] = w.w;
-      } else {
-        const uint2 w = reinterpret_cast<const uint2*>(shared)[at];
-        b[0] = w.x;
-        b[1] = w.y;
-      }
+      const uint2 w = shared[(ks * NT + n) * 32 + (threadIdx.x & 31)];
+      b[0] = w.x;
+      b[1] = w.y;
     } else {
-#pragma unroll
-      for (int i = 0; i < kQWords; ++i) b[i] = q[n][ks][i];
+      b[0] = q[n][ks][0];
+      b[1] = q[n][ks][1];
     }
   }
 
   // Address of 16-byte chunk c of row r in a tile: chunks are permuted within
-  // 128-byte lines so that the eight rows of an 8x8 matrix use all banks.
+  // 128-byte lines so that the eight rows of an 8x8 matrix use all banks, the
+  // rows 0-7 and 8-15 as well as the rows key_of(0-7) and key_of(8-15).
   static __device__ __forceinline__ uint32_t chunk_at(uint32_t tile, int r, int c) {
     if constexpr (S::kChunks == 4)
-      return tile + r * 64 + ((c ^ ((r >> 1) & 3)) << 4);
+      return tile + r * 64 + ((c ^ (((r >> 1) & 2) | (((r >> 1) ^ (r >> 3)) & 1))) << 4);
     else
-      return tile + r * S::kRowBytes + ((c ^ (r & 7)) << 4);
+      return tile + r * S::kRowBytes + ((c ^ (r & 7) ^ ((r >> 2) & 2)) << 4);
   }
 
   // One tile: scores, softmax, and the products with V.
   __device__ __forceinline__ void tile(uint32_t kt, uint32_t vt, const float* scales, uint32_t valid,
-                                       const uint4* shared_q) {
+                                       const uint2* shared_q) {
     const int lane = threadIdx.x & 31, g = lane >> 2;
     const float ninf = __int_as_float(0xff800000);
-    float s[NT][kGroups][4], low[NT][kE4m3 ? kGroups : 1][4];
+    float s[NT][kGroups][4];
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
       for (int k = 0; k < kGroups; ++k)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          s[n][k][i] = 0.0f;
-          if constexpr (kE4m3) low[n][k][i] = 0.0f;
-        }
+        for (int i = 0; i < 4; ++i) s[n][k][i] = 0.0f;
+    constexpr int kStepsPerLoad = kE4m3 ? 2 : 1;
 #pragma unroll
-    for (int ks = 0; ks < kSteps; ++ks) {
-      uint32_t b[NT][kQWords];
+    for (int ks = 0; ks < kSteps; ks += kStepsPerLoad) {
+      uint32_t b[kStepsPerLoad][NT][kQWords];
 #pragma unroll
-      for (int n = 0; n < NT; ++n) fragment(b[n], n, ks, shared_q);
+      for (int x = 0; x < kStepsPerLoad; ++x)
+#pragma unroll
+        for (int n = 0; n < NT; ++n) fragment(b[x][n], n, ks + x, shared_q);
 #pragma unroll
       for (int k = 0; k < kGroups; ++k) {
-        uint32_t a[4];
-        load_matrices(a, chunk_at(kt, k * 16 + (lane & 15), 2 * ks + (lane >> 4)));
+        uint32_t r[4];
+        load_matrices(r, chunk_at(kt, k * 16 + key_of(lane & 15), (kE4m3 ? ks : 2 * ks) + (lane >> 4)));
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
+        for (int x = 0; x < kStepsPerLoad; ++x) {
           if constexpr (kE4m3) {
-            mma16832_e4m3(s[n][k], a, b[n][0], b[n][1]);
-            mma16832_e4m3(low[n][k], a, b[n][kQWords - 2], b[n][kQWords - 1]);
+            const uint32_t a[4] = {e4m3x2_to_f16x2(r[2 * x] & 0xffffu), e4m3x2_to_f16x2(r[2 * x + 1] & 0xffffu),
+                                   e4m3x2_to_f16x2(r[2 * x] >> 16), e4m3x2_to_f16x2(r[2 * x + 1] >> 16)};
+#pragma unroll
+            for (int n = 0; n < NT; ++n) mma16816<true>(s[n][k], a, b[x][n][0], b[x][n][1]);
           } else {
-            mma16816<false>(s[n][k], a, b[n][0], b[n][1]);
+#pragma unroll
+            for (int n = 0; n < NT; ++n) mma16816<false>(s[n][k], r, b[x][n][0], b[x][n][1]);
           }
         }
       }
@@ -377,16 +364,16 @@ struct AttendWarp {
 #pragma unroll
     for (int k = 0; k < kGroups; ++k)
 #pragma unroll
-      for (int y = 0; y < 2; ++y) {  // key k * 16 + g + 8 y
+      for (int y = 0; y < 2; ++y) {
         float ks = 1.0f;
-        if constexpr (kE4m3) ks = scales[k * 16 + g + 8 * y];
+        if constexpr (kE4m3) ks = scales[k * 16 + key_of(g + 8 * y)];
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             float& x = s[n][k][2 * y + h];
             if constexpr (kE4m3)
-              x = fmaf(low[n][k][2 * y + h], 0.03125f, x) * ks * head_scale[n][h];
+              x *= ks * head_scale[n][h];
             else
               x *= head_scale[n][h];
           }
@@ -396,7 +383,7 @@ struct AttendWarp {
       for (int k = 0; k < kGroups; ++k)
 #pragma unroll
         for (int y = 0; y < 2; ++y)
-          if (!((valid >> (k * 16 + g + 8 * y)) & 1u))
+          if (!((valid >> (k * 16 + key_of(g + 8 * y))) & 1u))
 #pragma unroll
             for (int n = 0; n < NT; ++n) s[n][k][2 * y] = s[n][k][2 * y + 1] = ninf;
     }
@@ -457,7 +444,7 @@ struct AttendWarp {
       for (int k = 0; k < kGroups; ++k)
 #pragma unroll
         for (int y = 0; y < 2; ++y) {
-          const float vs = scales[S::kKeys + k * 16 + g + 8 * y];
+          const float vs = scales[S::kKeys + k * 16 + key_of(g + 8 * y)];
 #pragma unroll
           for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -522,13 +509,11 @@ struct AttendWarp {
 #pragma unroll
         for (int c = 0; c < S::kChunks; c += 2) {
           uint32_t r[4];
-          load_matrices_t(r, chunk_at(vt, k * 16 + (lane & 15), c + (lane >> 4)));
+          load_bytes_t(r, chunk_at(vt, k * 16 + (lane & 15), c + (lane >> 4)));
 #pragma unroll
-          for (int x = 0; x < 2; ++x) {  // chunk c + x: its even columns as rows 0-7, its odd ones as rows 8-15
-            const uint32_t a[4] = {
-                e4m3x2_to_f16x2(__byte_perm(r[2 * x], 0, 0x4420)), e4m3x2_to_f16x2(__byte_perm(r[2 * x], 0, 0x4431)),
-                e4m3x2_to_f16x2(__byte_perm(r[2 * x + 1], 0, 0x4420)),
-                e4m3x2_to_f16x2(__byte_perm(r[2 * x + 1], 0, 0x4431))};
+          for (int x = 0; x < 2; ++x) {
+            const uint32_t a[4] = {e4m3x2_to_f16x2(r[2 * x] & 0xffffu), e4m3x2_to_f16x2(r[2 * x + 1] & 0xffffu),
+                                   e4m3x2_to_f16x2(r[2 * x] >> 16), e4m3x2_to_f16x2(r[2 * x + 1] >> 16)};
 #pragma unroll
             for (int n = 0; n < NT; ++n) mma16816<true>(o[n][c + x], a, hi[n][0], hi[n][1]);
           }
@@ -549,9 +534,7 @@ struct AttendWarp {
   }
 
   // Column of o[.][j][i] for a lane with lane / 4 = g.
-  static __device__ __forceinline__ int column(int j, int i, int g) {
-    return kE4m3 ? 16 * j + 2 * g + (i >> 1) : 16 * j + g + 8 * (i >> 1);
-  }
+  static __device__ __forceinline__ int column(int j, int i, int g) { return 16 * j + g + 8 * (i >> 1); }
 };
 
 // ---------------------------------------------------------------- joining
@@ -641,7 +624,7 @@ __global__ void __launch_bounds__(kAttendThreads, (AttendShape<D, kE4m3, NT>::kC
   extern __shared__ __align__(128) unsigned char smem[];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   float* join = reinterpret_cast<float*>(smem + S::kOffJoin);
-  uint4* shared_q = reinterpret_cast<uint4*>(smem + S::kOffQ);
+  uint2* shared_q = reinterpret_cast<uint2*>(smem + S::kOffQ);
   float* ml = reinterpret_cast<float*>(smem + S::kOffMl);  // [warp][m of 16 rows, l of 16 rows]
   uint32_t* valid_masks = reinterpret_cast<uint32_t*>(smem + S::kOffValid) + warp * S::kStages;
   int64_t* plan = reinterpret_cast<int64_t*>(smem + S::kOffPlan);
