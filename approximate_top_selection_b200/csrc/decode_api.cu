@@ -21,7 +21,7 @@ namespace {
 
 // The part of a workspace that is zero between calls, of every operator.
 constexpr size_t kTicketBytes = TOPK_DECODE_TICKET_BYTES;
-static_assert(kTicketBytes >= 4 * kAttendMaxCtas && kTicketBytes >= 4 * kBeamTickets, "tickets");
+static_assert(kTicketBytes >= 12 * kAttendMaxCtas && kTicketBytes >= 4 * kBeamTickets, "tickets");
 
 constexpr int kMaxReorder = 256;
 constexpr int64_t kMaxGridX = 2147483647LL;
@@ -79,8 +79,8 @@ int table_view(const int32_t* table, int64_t stride, int width, const int32_t* l
 }
 
 // CTAs of the attention's line: all that are resident at once.  The workspace
-// is sized for two per SM, the most any instantiation has.
-constexpr int kAttendCtasPerSm = 2;
+// is sized for three per SM, the most any instantiation has.
+constexpr int kAttendCtasPerSm = 3;
 
 size_t attend_workspace(int d, const DeviceInfo& dev) {
   const int ctas = std::min(dev.sms * kAttendCtasPerSm, kAttendMaxCtas);
@@ -243,7 +243,7 @@ int paged_attention(const uint16_t* q, int64_t q_stride, int64_t batch, int head
   while ((1LL << (a.page_shift - 31)) < k_cache->page_size) ++a.page_shift;
   a.page_magic = static_cast<uint32_t>(((static_cast<unsigned __int128>(1) << a.page_shift) + k_cache->page_size - 1) /
                                        static_cast<unsigned>(k_cache->page_size));
-  a.grouped = !positions && k_cache->page_size % 16 == 0;
+  a.grouped = !positions && k_cache->page_size % 16 == 0 && a.same_strides;
   a.q = q;
   a.q_stride = q_stride;
   a.positions = positions;

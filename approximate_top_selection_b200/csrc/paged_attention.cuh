@@ -20,10 +20,14 @@
 // that finishes last (an atomic ticket, nobody waits; the parts are added in
 // the order of the CTAs, so equal calls give equal bits).
 //
-// Each warp feeds itself: its lanes look up its tile's rows (a position, then
-// a page, each a tile ahead of its use) and copy them by 16-byte cp.async into
-// a ring of STAGES tiles of its own, so no barrier of the CTA stands in the
-// loop and any page size, stride or list of positions costs the same.
+// Each warp feeds itself through a ring of STAGES tiles of its own, so no
+// barrier of the CTA stands in the loop and any page size, stride or list of
+// positions is served.  A tile goes through three steps, STAGES - 1 tiles
+// apart: its tokens (a list's positions are copied), its pages (looked up in
+// the block table), its rows.  All three are cp.async copies into shared memory
+// in the groups that the ring waits for anyway, so neither look-up's latency is
+// ever waited for by itself (with look-ups one tile ahead in registers they took
+// twice the time of the products on lists of 512 positions).
 #pragma once
 
 #include "kv_cache.cuh"
@@ -39,12 +43,12 @@ struct AttendArgs {
   int heads, lists, c;
   int row_tiles;      // groups of 16 query heads per list
   uint32_t page_magic, page_shift;  // t / page_size = (t * page_magic) >> page_shift for 0 <= t < 2^31
-  bool grouped;       // no positions, and 16 | page_size: 16 tokens from a multiple of 16 on share a page
+  bool grouped;       // no positions, 16 | page_size (16 tokens from a multiple of 16 on share a page), same strides
   bool same_strides;  // k and v have equal strides
   float scale_log2;   // softmax scale * log2(e)
   uint16_t* out;      // [batch][heads][d] bf16
   float* lse;         // null, or [batch][heads]
-  uint32_t* tickets;  // [kAttendMaxCtas], zero between calls
+  uint32_t* tickets;  // [kAttendMaxCtas] of units by first CTA, [2 kAttendMaxCtas] of groups; zero between calls
   float* parts;       // [ctas][2][16 * (d + 2)]
 };
 
@@ -59,23 +63,33 @@ struct AttendShape {
   static constexpr int kRowBytes = D * (kE4m3 ? 1 : 2);
   static constexpr int kChunks = kRowBytes / 16;
   static constexpr int kKeys = D == 256 ? 16 : (D == 128 && !kE4m3) ? 16 : 32;  // per warp tile
+  static constexpr uint32_t kAllKeys = kKeys == 32 ? 0xffffffffu : (1u << (kKeys & 31)) - 1u;
   static constexpr int kGranule = kAttendWarps * kKeys;
   static constexpr int kTileBytes = kKeys * kRowBytes;               // K or V
   static constexpr int kScaleBytes = kE4m3 ? 2 * kKeys * 4 : 0;
   static constexpr int kStageBytes = 2 * kTileBytes + kScaleBytes;
   static constexpr bool kQShared = D == 256 && NT == 2;  // Q fragments in shared memory (64 registers otherwise)
-  // 8 KB a tile: three stages of four warps and two CTAs fill an SM's shared memory
-  static constexpr int kCtasPerSm = D == 256 && (!kE4m3 || NT == 2) ? 1 : 2;
-  static constexpr int kStages = D == 64 && kE4m3 ? 6 : D == 256 && kE4m3 && NT == 2 ? 5 : 3;
-  static constexpr int kJoinFloats = 2304;
-  // shared memory: [warps][stages] tiles, join buffer, Q fragments, (m, l) per warp and joined, valid masks, plan
+  // About 8 KB a tile: three stages of four warps and two CTAs fill an SM's
+  // shared memory.  Tiles that take more instructions for their bytes (e4m3, or
+  // narrow rows) gain more by a third CTA than by a third stage.
+  static constexpr bool kThree = NT == 1 && (D == 64 || (D == 128 && kE4m3));
+  static constexpr int kCtasPerSm = kThree ? 3 : D == 256 && (!kE4m3 || NT == 2) ? 1 : 2;
+  static constexpr int kStages = D == 64 && kE4m3 ? (kThree ? 3 : 5) : kThree ? 2 : D == 256 && kE4m3 && NT == 2 ? 5 : 3;
+  static constexpr int kSlots = 2 * kStages - 1;  // tiles from their tokens to their rows
+  static constexpr int kJoinFloats = kThree ? 1280 : 1792;
+  // shared memory: [warps][stages] tiles, join buffer, Q fragments, (m, l) per warp and joined,
+  // [warps][slots] tokens, pages and places, [warps][stages] valid masks, plan
   static constexpr int kOffJoin = kAttendWarps * kStages * kStageBytes;
   static constexpr int kOffQ = kOffJoin + kJoinFloats * 4;
   static constexpr int kOffMl = kOffQ + (kQShared ? 8192 : 0);
-  static constexpr int kOffValid = kOffMl + (kAttendWarps + 1) * 32 * 4;
-  static constexpr int kOffPlan = kOffValid + kAttendWarps * kStages * 4;
-  static constexpr int kSmem = (kOffPlan + 64 + 127) / 128 * 128;
-  static_assert(kOffPlan % 8 == 0, "plan alignment");
+  static constexpr int kOffPlace = kOffMl + (kAttendWarps + 1) * 32 * 4;
+  static constexpr int kOffToken = kOffPlace + kAttendWarps * kSlots * 16;
+  static constexpr int kOffPage = kOffToken + kAttendWarps * kSlots * kKeys * 4;
+  static constexpr int kOffPlan = kOffPage + kAttendWarps * kSlots * kKeys * 4;
+  static constexpr int kOffValid = kOffPlan + 64;
+  static constexpr int kSmem = (kOffValid + kAttendWarps * kStages * 4 + 127) / 128 * 128;
+  static_assert(kOffPlan % 8 == 0 && kOffPlace % 16 == 0, "alignment");
+  static_assert((kSmem + 1024) * kCtasPerSm <= 228 * 1024, "shared memory");
   // Columns of O joined at a time: 4 warps x rows x (columns + 4) floats fit
   // the buffer; the 4 spread a lane quad's heads over the banks.
   static __device__ __forceinline__ int join_columns(int rows) {
@@ -87,6 +101,9 @@ struct AttendShape {
 __device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool live) {
   const int bytes = live ? 16 : 0;  // the rest of the 16 is filled with zeros
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
 __device__ __forceinline__ void copy4(uint32_t dst, const void* src, bool live) {
   const int bytes = live ? 4 : 0;
@@ -214,7 +231,8 @@ struct AttendWarp {
 
   float o[NT][D / 16][4];
   float m[NT][2], l[NT][2];
-  float f[NT][2];  // e4m3: O holds sum w_j V8_j / f, with w_j = 2^(s_j - m) * vscale_j
+  float f[NT][2];    // e4m3: O holds sum w_j V8_j / f, with w_j = 2^(s_j - m) * vscale_j
+  float inv[NT][2];  // 1 / f
   uint32_t q[NT][S::kQShared ? 1 : kSteps][kQWords];
   float head_scale[NT][2];  // score in log2 units per unit of the product
 
@@ -229,10 +247,13 @@ struct AttendWarp {
       for (int h = 0; h < 2; ++h) {
         m[n][h] = __int_as_float(0xff800000);
         l[n][h] = 0.0f;
-        f[n][h] = 0.0f;
+        f[n][h] = inv[n][h] = 0.0f;
       }
     }
   }
+
+  // Weights below 2^-126 count as nothing.
+  static __device__ __forceinline__ float inverse(float f) { return f >= 1.2e-38f ? 1.0f / f : 0.0f; }
 
   static __device__ __forceinline__ int key_of(int r) {
     return kE4m3 ? ((r & 6) << 1) + (r & 1) + ((r >> 2) & 2) : r;
@@ -349,8 +370,9 @@ struct AttendWarp {
 #pragma unroll
         for (int x = 0; x < kStepsPerLoad; ++x) {
           if constexpr (kE4m3) {
-            const uint32_t a[4] = {e4m3x2_to_f16x2(r[2 * x] & 0xffffu), e4m3x2_to_f16x2(r[2 * x + 1] & 0xffffu),
-                                   e4m3x2_to_f16x2(r[2 * x] >> 16), e4m3x2_to_f16x2(r[2 * x + 1] >> 16)};
+            uint32_t a[4];
+            e4m3x4_to_f16x2(r[2 * x], a[0], a[2]);
+            e4m3x4_to_f16x2(r[2 * x + 1], a[1], a[3]);
 #pragma unroll
             for (int n = 0; n < NT; ++n) mma16816<true>(s[n][k], a, b[x][n][0], b[x][n][1]);
           } else {
@@ -378,7 +400,7 @@ struct AttendWarp {
               x *= head_scale[n][h];
           }
       }
-    if (valid != (S::kKeys == 32 ? 0xffffffffu : (1u << (S::kKeys & 31)) - 1u)) {
+    if (valid != S::kAllKeys) {
 #pragma unroll
       for (int k = 0; k < kGroups; ++k)
 #pragma unroll
@@ -412,6 +434,7 @@ struct AttendWarp {
           l[n][h] *= x;
           if constexpr (kE4m3) {
             f[n][h] *= x;
+            inv[n][h] = inverse(f[n][h]);
           } else {
 #pragma unroll
             for (int j = 0; j < D / 16; ++j) {
@@ -466,6 +489,7 @@ struct AttendWarp {
             const float fn = fmaxf(f[n][h], fminf(column_max(wt[n][h]), 1e36f));
             const float x = fn > 0.0f ? f[n][h] / fn : 0.0f;
             f[n][h] = fn;
+            inv[n][h] = inverse(fn);
 #pragma unroll
             for (int j = 0; j < D / 16; ++j) {
               o[n][j][h] *= x;
@@ -477,11 +501,10 @@ struct AttendWarp {
       for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          const float inv = f[n][h] >= 1.2e-38f ? 1.0f / f[n][h] : 0.0f;  // weights below 2^-126 count as nothing
 #pragma unroll
           for (int k = 0; k < kGroups; ++k) {
-            s[n][k][h] *= inv;
-            s[n][k][2 + h] *= inv;
+            s[n][k][h] *= inv[n][h];
+            s[n][k][2 + h] *= inv[n][h];
           }
         }
     }
@@ -512,8 +535,9 @@ struct AttendWarp {
           load_bytes_t(r, chunk_at(vt, k * 16 + (lane & 15), c + (lane >> 4)));
 #pragma unroll
           for (int x = 0; x < 2; ++x) {
-            const uint32_t a[4] = {e4m3x2_to_f16x2(r[2 * x] & 0xffffu), e4m3x2_to_f16x2(r[2 * x + 1] & 0xffffu),
-                                   e4m3x2_to_f16x2(r[2 * x] >> 16), e4m3x2_to_f16x2(r[2 * x + 1] >> 16)};
+            uint32_t a[4];
+            e4m3x4_to_f16x2(r[2 * x], a[0], a[2]);
+            e4m3x4_to_f16x2(r[2 * x + 1], a[1], a[3]);
 #pragma unroll
             for (int n = 0; n < NT; ++n) mma16816<true>(o[n][c + x], a, hi[n][0], hi[n][1]);
           }
@@ -538,81 +562,111 @@ struct AttendWarp {
 };
 
 // ---------------------------------------------------------------- joining
-// Joins the parts of a unit that lies in CTAs first .. last (in that order)
-// and writes its rows.  All threads of the CTA.
+// The part of a unit that CTA c holds: its first CTA writes slot 1, the others
+// (which continue a unit) slot 0.  m of 16 rows, l of 16 rows, O [16][D].
 template <int D>
-__device__ void attend_join(const AttendArgs& p, int first, int last, int rows, int64_t out_row, float* buf) {
-  constexpr int V = D / 32;  // columns per lane
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int per_row = rows == 1 ? 4 : rows == 2 ? 2 : 1;  // warps that share a row's parts
-  const float ninf = __int_as_float(0xff800000);
-  const int n = last - first + 1;
-  for (int base = 0; base < rows; base += kAttendWarps / per_row) {
-    const int row = base + warp / per_row, sub = warp % per_row;
-    float acc[V], total = 0.0f, mm = ninf;
-#pragma unroll
-    for (int i = 0; i < V; ++i) acc[i] = 0.0f;
-    if (row < rows) {
-      for (int i = lane; i < n; i += 32)
-        mm = fmaxf(mm, __ldcg(p.parts + static_cast<int64_t>((first + i) * 2 + (i == 0)) * attend_part_floats(D) + row));
-#pragma unroll
-      for (int x = 16; x; x >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, x));
-      const float ref = finite_or_zero(mm);
-      for (int i0 = sub * 32; i0 < n; i0 += per_row * 32) {
-        const int i = i0 + lane;
-        float w = 0.0f;
-        if (i < n) {
-          const float* part = p.parts + static_cast<int64_t>((first + i) * 2 + (i == 0)) * attend_part_floats(D);
-          w = exp2_fast(__ldcg(part + row) - ref);
-          total += w * __ldcg(part + 16 + row);
-        }
-        const int m = min(32, n - i0);
-#pragma unroll 8
-        for (int x = 0; x < m; ++x) {
-          const float wx = __shfl_sync(0xffffffffu, w, x);
-          const float* src = p.parts +
-                             static_cast<int64_t>((first + i0 + x) * 2 + (i0 + x == 0)) * attend_part_floats(D) + 32 +
-                             row * D + lane * V;
-          if constexpr (V == 2) {
-            const float2 a = __ldcg(reinterpret_cast<const float2*>(src));
-            acc[0] += wx * a.x;
-            acc[1] += wx * a.y;
-          } else {
-#pragma unroll
-            for (int y = 0; y < V; y += 4) {
-              const float4 a = __ldcg(reinterpret_cast<const float4*>(src + y));
-              acc[y] += wx * a.x;
-              acc[y + 1] += wx * a.y;
-              acc[y + 2] += wx * a.z;
-              acc[y + 3] += wx * a.w;
-            }
-          }
-        }
-      }
-#pragma unroll
-      for (int x = 16; x; x >>= 1) total += __shfl_xor_sync(0xffffffffu, total, x);
+__device__ __forceinline__ float* attend_part(float* parts, int c, int first) {
+  return parts + static_cast<int64_t>(c * 2 + (c == first)) * attend_part_floats(D);
+}
+
+// Joins the n (up to 32) parts of CTAs c0, c0 + step, ... in that order: into
+// the unit's output rows, or into the first of the parts.  All threads of the
+// CTA; buf holds 1056 floats.  (A call of its own; it takes no reference to the
+// kernel's arguments, which would move them from constant to local memory.)
+template <int D>
+__device__ __noinline__ void attend_join(float* parts, int first, int c0, int n, int step, int rows, bool final,
+                                         uint16_t* out, float* lse, float* buf) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  float* weight = buf;        // [rows][32]
+  float* mass = buf + 512;    // [rows] max, [rows] sum
+  float* half = buf + 544;    // [<= 128][4] partial sums
+  for (int r = warp; r < rows; r += kAttendWarps) {
+    float m = __int_as_float(0xff800000), l = 0.0f;
+    if (lane < n) {
+      const float* part = attend_part<D>(parts, c0 + lane * step, first);
+      m = __ldcg(part + r);
+      l = __ldcg(part + 16 + r);
     }
-    if (per_row > 1) {  // the row's warps meet in shared memory, added in warp order
-      __syncthreads();
+    float mm = m;
 #pragma unroll
-      for (int i = 0; i < V; ++i) buf[warp * D + lane * V + i] = acc[i];
-      if (lane == 0) buf[4 * D + warp] = total;
-      __syncthreads();
-      if (sub == 0)
-        for (int w = 1; w < per_row; ++w) {
+    for (int x = 16; x; x >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, x));
+    const float w = exp2_fast(m - finite_or_zero(mm));
+    float sum = lane < n ? w * l : 0.0f;
 #pragma unroll
-          for (int i = 0; i < V; ++i) acc[i] += buf[(warp + w) * D + lane * V + i];
-          total += buf[4 * D + warp + w];
-        }
-    }
-    if (row < rows && sub == 0) {
-      const float inv = total == 0.0f ? 0.0f : 1.0f / total;
-      uint32_t* dst = reinterpret_cast<uint32_t*>(p.out + (out_row + row) * D + lane * V);
-#pragma unroll
-      for (int i = 0; i < V; i += 2) dst[i / 2] = floats_to_bf16x2(acc[i] * inv, acc[i + 1] * inv);
-      if (p.lse && lane == 0) p.lse[out_row + row] = 0.6931471805599453f * (mm + log2f(total));
+    for (int x = 16; x; x >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
+    weight[r * 32 + lane] = w;
+    if (lane == 0) {
+      mass[r] = mm;
+      mass[16 + r] = sum;
     }
   }
+  __syncthreads();
+  // Four columns of a row per thread; few rows share their parts out to
+  // `split` threads, added in order.
+  const int total = rows * (D / 4);
+  const int split = total > 64 ? 1 : total > 32 ? 2 : 4;
+  float* dst0 = attend_part<D>(parts, c0, first);
+  for (int i0 = 0; i0 < total; i0 += kAttendThreads / split) {
+    const int i = i0 + tid % (kAttendThreads / split), s = tid / (kAttendThreads / split);
+    const int r = i / (D / 4), col = i % (D / 4) * 4;
+    float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    if (i < total) {
+#pragma unroll 8
+      for (int x = s; x < n; x += split) {
+        const float w = weight[r * 32 + x];
+        const float4 v =
+            __ldcg(reinterpret_cast<const float4*>(attend_part<D>(parts, c0 + x * step, first) + 32 + r * D + col));
+        acc.x += w * v.x;
+        acc.y += w * v.y;
+        acc.z += w * v.z;
+        acc.w += w * v.w;
+      }
+    }
+    if (split > 1) {
+      reinterpret_cast<float4*>(half)[tid] = acc;
+      __syncthreads();
+      if (s == 0)
+        for (int x = 1; x < split; ++x) {
+          const float4 v = reinterpret_cast<const float4*>(half)[tid + x * (kAttendThreads / split)];
+          acc.x += v.x;
+          acc.y += v.y;
+          acc.z += v.z;
+          acc.w += v.w;
+        }
+    }
+    if (i < total && s == 0) {
+      if (final) {
+        const float inv = mass[16 + r] == 0.0f ? 0.0f : 1.0f / mass[16 + r];
+        *reinterpret_cast<uint2*>(out + r * D + col) =
+            make_uint2(floats_to_bf16x2(acc.x * inv, acc.y * inv), floats_to_bf16x2(acc.z * inv, acc.w * inv));
+      } else {
+        *reinterpret_cast<float4*>(dst0 + 32 + r * D + col) = acc;  // read by this thread alone
+      }
+    }
+  }
+  if (tid < rows) {
+    if (final) {
+      if (lse) lse[tid] = 0.6931471805599453f * (mass[tid] + log2f(mass[16 + tid]));
+    } else {
+      dst0[tid] = mass[tid];
+      dst0[16 + tid] = mass[16 + tid];
+    }
+  }
+}
+
+// One of `count` arrivals at a ticket; true for all threads of the CTA that
+// arrives last, which then sees what the others wrote before they arrived.
+__device__ __forceinline__ bool attend_arrive(uint32_t* ticket, int count, int64_t* flag) {
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    __threadfence();
+    const bool last = atomicAdd(ticket, 1u) == static_cast<uint32_t>(count - 1);
+    if (last) *ticket = 0;
+    __threadfence();
+    *flag = last;
+  }
+  __syncthreads();
+  return *flag != 0;
 }
 
 // ---------------------------------------------------------------- kernel
@@ -627,6 +681,9 @@ __global__ void __launch_bounds__(kAttendThreads, (AttendShape<D, kE4m3, NT>::kC
   uint2* shared_q = reinterpret_cast<uint2*>(smem + S::kOffQ);
   float* ml = reinterpret_cast<float*>(smem + S::kOffMl);  // [warp][m of 16 rows, l of 16 rows]
   uint32_t* valid_masks = reinterpret_cast<uint32_t*>(smem + S::kOffValid) + warp * S::kStages;
+  int4* places = reinterpret_cast<int4*>(smem + S::kOffPlace) + warp * S::kSlots;
+  int* tokens = reinterpret_cast<int*>(smem + S::kOffToken) + warp * S::kSlots * S::kKeys;
+  int* pages = reinterpret_cast<int*>(smem + S::kOffPage) + warp * S::kSlots * S::kKeys;
   int64_t* plan = reinterpret_cast<int64_t*>(smem + S::kOffPlan);
   unsigned char* ring = smem + warp * S::kStages * S::kStageBytes;
   const uint32_t ring_addr = smem_addr(ring);
@@ -706,50 +763,64 @@ __global__ void __launch_bounds__(kAttendThreads, (AttendShape<D, kE4m3, NT>::kC
   }
   if (g0 >= g1) return;
 
-  // The three steps of a tile's rows, each a tile behind the one before: the
-  // lane's token, its page, the copies.  A lane of index < kKeys has a key.
+  // The three steps of a tile.  A lane of index < kKeys has a key.  Where a
+  // tile lies: its sequence, its key-value head, the sequence's length and the
+  // first of its tokens (or -1 behind the share's end).
   AttendCursor ahead = cur;
   int64_t ahead_left = g1 - g0;
-  int tok = -1, tok_b = 0, tok_kv = 0, tok_len = 0;
-  int32_t page = -1;
-  int off = 0, page_kv = 0;
   const int kv_per = p.lists / p.k.kv_heads;
-  auto next_token = [&]() {
-    tok = -1;
+  const uint32_t tokens_addr = smem_addr(tokens), pages_addr = smem_addr(pages);
+  auto fetch_tokens = [&](int slot) {
+    int4 place = make_int4(0, 0, 0, -1);
     if (ahead_left > 0) {
-      const uint32_t i = (static_cast<uint32_t>(ahead.at) * kAttendWarps + warp) * S::kKeys + lane;
+      const uint32_t i0 = (static_cast<uint32_t>(ahead.at) * kAttendWarps + warp) * S::kKeys;
       const int list = ahead.unit / p.row_tiles;
-      tok_b = ahead.b;
-      tok_kv = list / kv_per;
-      tok_len = p.positions ? seq_length(p.tab, ahead.b) : ahead.count;
-      if (lane < S::kKeys && i < static_cast<uint32_t>(ahead.count))
-        tok = p.positions ? __ldg(p.positions + (static_cast<int64_t>(ahead.b) * p.lists + list) * p.c + i) : static_cast<int>(i);
+      const int len = p.positions ? seq_length(p.tab, ahead.b) : ahead.count;
+      place = make_int4(ahead.b, list / kv_per, len, static_cast<int>(min(i0, 0x7fffffffu)));
+      if (p.positions && lane < S::kKeys) {
+        const bool on = i0 + lane < static_cast<uint32_t>(ahead.count);
+        copy4(tokens_addr + (slot * S::kKeys + lane) * 4,
+              p.positions + (static_cast<int64_t>(ahead.b) * p.lists + list) * p.c + (on ? i0 + lane : 0), on);
+      }
       --ahead_left;
       cursor_next<S::kGranule>(p, ahead);
     }
+    if (lane == 0) places[slot] = place;
   };
-  auto next_page = [&]() {
-    page = -1;
-    page_kv = tok_kv;
-    if (tok >= 0) {
-      if (tok < tok_len) {
-        const int at = static_cast<int>((static_cast<uint64_t>(tok) * p.page_magic) >> p.page_shift);
-        off = tok - at * p.k.page_size;
-        page = __ldg(p.tab.table + tok_b * p.tab.stride + at);
-        if (page < 0 || page >= p.k.pages) {
-          atomicOr(&g_device_status, kDevBadIndex);
-          page = -1;
-        }
-      } else if (tok >= p.tab.capacity) {
+  // The lane's token, or -1 (a list's slots behind its end were filled with
+  // zeros by the copy, so they are told by their index).
+  auto token_of = [&](int slot, const int4& place) {
+    if (place.w < 0 || lane >= S::kKeys) return -1;
+    const uint32_t i = static_cast<uint32_t>(place.w) + lane;
+    if (!p.positions) return i < static_cast<uint32_t>(place.z) ? static_cast<int>(i) : -1;
+    return i < static_cast<uint32_t>(p.c) ? tokens[slot * S::kKeys + lane] : -1;
+  };
+  auto fetch_pages = [&](int slot) {
+    const int4 place = places[slot];
+    const int tok = token_of(slot, place);
+    const bool on = tok >= 0 && tok < place.z;
+    if (tok >= p.tab.capacity) atomicOr(&g_device_status, kDevBadIndex);
+    const int64_t at = on ? static_cast<int64_t>((static_cast<uint64_t>(tok) * p.page_magic) >> p.page_shift) : 0;
+    if (lane < S::kKeys) copy4(pages_addr + (slot * S::kKeys + lane) * 4, p.tab.table + place.x * p.tab.stride + at, on);
+  };
+  auto fetch_rows = [&](int stage, int slot) {
+    const int4 place = places[slot];
+    const int tok = token_of(slot, place);
+    bool live = tok >= 0 && tok < place.z;
+    int64_t pg = 0;
+    int o = 0;
+    if (live) {
+      pg = pages[slot * S::kKeys + lane];
+      o = tok - static_cast<int>((static_cast<uint64_t>(tok) * p.page_magic) >> p.page_shift) * p.k.page_size;
+      if (pg < 0 || pg >= p.k.pages) {
         atomicOr(&g_device_status, kDevBadIndex);
+        live = false;
+        pg = 0;
+        o = 0;
       }
     }
-  };
-  auto issue = [&](int stage) {
-    const bool live = page >= 0;
     const uint32_t valid = __ballot_sync(0xffffffffu, live);
-    const int64_t pg = live ? page : 0;
-    const int o = live ? off : 0;
+    const int page_kv = place.y;
     const int64_t ko = pg * p.k.page_stride + page_kv * p.k.head_stride + o * p.k.token_stride;
     int64_t vo = ko;
     if (!p.same_strides) vo = pg * p.v.page_stride + page_kv * p.v.head_stride + o * p.v.token_stride;
@@ -758,28 +829,50 @@ __global__ void __launch_bounds__(kAttendThreads, (AttendShape<D, kE4m3, NT>::kC
     if (valid) {
       constexpr int kRowsPerCopy = 32 / S::kChunks;
       const int c = lane % S::kChunks, r0 = lane / S::kChunks;
-      if (p.grouped && p.same_strides) {  // one address for 16 rows of K and of V
+      if (p.grouped && valid == S::kAllKeys) {
+        // The common tile: one address for 16 rows of K and of V, no row left
+        // out.  r0 is below the power of two kRowsPerCopy, so that the chunk's
+        // permutation is the lane's own and a constant of the copy.
+        const uint32_t lane_at = W::chunk_at(0, r0, c);
+        const int64_t step = kRowsPerCopy * p.k.token_stride;
+        const int64_t lane_off = r0 * p.k.token_stride + c * 16;
 #pragma unroll
         for (int y = 0; y < S::kKeys / 16; ++y) {
-          int64_t a = __shfl_sync(0xffffffffu, ko, y * 16) + r0 * p.k.token_stride + c * 16;
+          const int64_t a = __shfl_sync(0xffffffffu, ko, y * 16) + lane_off;
+          const unsigned char* ka = p.k.data + a;
+          const unsigned char* va = p.v.data + a;
 #pragma unroll
           for (int i = 0; i < 16 / kRowsPerCopy; ++i) {
-            const int r = y * 16 + i * kRowsPerCopy + r0;
-            const bool on = (valid >> r) & 1u;
-            copy16(W::chunk_at(kt, r, c), p.k.data + a, on);
-            copy16(W::chunk_at(vt, r, c), p.v.data + a, on);
-            a += kRowsPerCopy * p.k.token_stride;
+            const uint32_t flip = W::chunk_at(0, y * 16 + i * kRowsPerCopy, 0);
+            copy16(kt + ((lane_at ^ (flip & 127)) + (flip & ~127u)), ka);
+            copy16(vt + ((lane_at ^ (flip & 127)) + (flip & ~127u)), va);
+            ka += step;
+            va += step;
           }
         }
       } else {
+        // any rows: their addresses from the lanes that looked them up, a few
+        // rows at a time so that the exchanges overlap
+        constexpr int kCopies = S::kKeys / kRowsPerCopy, kBatch = kCopies < 8 ? kCopies : 8;
 #pragma unroll
-        for (int i = 0; i < S::kKeys / kRowsPerCopy; ++i) {
-          const int r = i * kRowsPerCopy + r0;
-          const int64_t a = __shfl_sync(0xffffffffu, ko, r) + c * 16;
-          const bool on = (valid >> r) & 1u;
-          copy16(W::chunk_at(kt, r, c), p.k.data + a, on);
-          const int64_t b = p.same_strides ? a : __shfl_sync(0xffffffffu, vo, r) + c * 16;
-          copy16(W::chunk_at(vt, r, c), p.v.data + b, on);
+        for (int i0 = 0; i0 < kCopies; i0 += kBatch) {
+          int64_t at[kBatch];
+#pragma unroll
+          for (int i = 0; i < kBatch; ++i) at[i] = __shfl_sync(0xffffffffu, ko, (i0 + i) * kRowsPerCopy + r0) + c * 16;
+#pragma unroll
+          for (int i = 0; i < kBatch; ++i) {
+            const int r = (i0 + i) * kRowsPerCopy + r0;
+            copy16(W::chunk_at(kt, r, c), p.k.data + at[i], (valid >> r) & 1u);
+          }
+          if (!p.same_strides) {
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) at[i] = __shfl_sync(0xffffffffu, vo, (i0 + i) * kRowsPerCopy + r0) + c * 16;
+          }
+#pragma unroll
+          for (int i = 0; i < kBatch; ++i) {
+            const int r = (i0 + i) * kRowsPerCopy + r0;
+            copy16(W::chunk_at(vt, r, c), p.v.data + at[i], (valid >> r) & 1u);
+          }
         }
       }
       if constexpr (kE4m3) {
@@ -791,17 +884,41 @@ __global__ void __launch_bounds__(kAttendThreads, (AttendShape<D, kE4m3, NT>::kC
         }
       }
     }
-    copy_commit();
   };
 
-  next_token();
-  next_page();
-  next_token();
+  // Before the first tile: its tokens, and those of the tiles that the steps
+  // are apart; then the pages likewise; then rows.  Slot of tile i: i % kSlots.
+  constexpr int kApart = S::kStages - 1;
+  int slot_t = 0, slot_p = 0, slot_r = 0;
+  auto next_slot = [](int& x) { x = x == S::kSlots - 1 ? 0 : x + 1; };
 #pragma unroll 1
-  for (int i = 0; i < S::kStages - 1; ++i) {
-    issue(i);
-    next_page();
-    next_token();
+  for (int i = 0; i < kApart; ++i) {
+    fetch_tokens(slot_t);
+    next_slot(slot_t);
+  }
+  copy_commit();
+  copy_wait<0>();
+  __syncwarp();
+#pragma unroll 1
+  for (int i = 0; i < kApart; ++i) {
+    fetch_pages(slot_p);
+    next_slot(slot_p);
+    fetch_tokens(slot_t);
+    next_slot(slot_t);
+  }
+  copy_commit();
+  copy_wait<0>();
+  __syncwarp();
+#pragma unroll 1
+  for (int i = 0; i < kApart; ++i) {
+    fetch_rows(i, slot_r);
+    next_slot(slot_r);
+    fetch_pages(slot_p);
+    next_slot(slot_p);
+    __syncwarp();  // the tokens' slot held the rows' place
+    fetch_tokens(slot_t);
+    next_slot(slot_t);
+    copy_commit();
   }
 
   W w;
@@ -821,12 +938,15 @@ __global__ void __launch_bounds__(kAttendThreads, (AttendShape<D, kE4m3, NT>::kC
     }
     copy_wait<S::kStages - 2>();
     __syncwarp();
-    {  // the stage consumed last is free again
-      const int s = stage == 0 ? S::kStages - 1 : stage - 1;
-      issue(s);
-      next_page();
-      next_token();
-    }
+    // the stage consumed last is free again, and so is the slot of its rows
+    fetch_rows(stage == 0 ? S::kStages - 1 : stage - 1, slot_r);
+    next_slot(slot_r);
+    fetch_pages(slot_p);
+    next_slot(slot_p);
+    __syncwarp();
+    fetch_tokens(slot_t);
+    next_slot(slot_t);
+    copy_commit();
     const uint32_t valid = valid_masks[stage];
     if (valid) {
       const uint32_t kt = ring_addr + stage * S::kStageBytes;
@@ -916,20 +1036,30 @@ __global__ void __launch_bounds__(kAttendThreads, (AttendShape<D, kE4m3, NT>::kC
       }
     }
     if (!whole) {
+      // Up to 32 parts are joined at once; more by groups of 32, and then the
+      // groups (one CTA reading hundreds of parts would take longer than the
+      // cache did).
       const int first = part_of(unit_first, total, ctas, 1);
       const int last = part_of(unit_first + cur.granules - 1, total, ctas, 1);
-      __threadfence();
-      __syncthreads();
-      if (tid == 0) {
-        const uint32_t n = static_cast<uint32_t>(last - first);
-        const bool done = atomicAdd(p.tickets + first, 1u) == n;
-        if (done) p.tickets[first] = 0;
-        plan[6] = done;
+      const int n = last - first + 1, me = static_cast<int>(blockIdx.x) - first;
+      uint16_t* out = p.out + out_row * D;
+      float* lse = p.lse ? p.lse + out_row : nullptr;
+      // one call site: the whole unit's parts, a group's, or the groups'
+      int c0 = first, members = n, step = 1;
+      uint32_t* ticket = p.tickets + first;
+      if (n > 32) {
+        c0 = first + me / 32 * 32;
+        members = min(32, last - c0 + 1);
+        ticket = p.tickets + kAttendMaxCtas + 2 * c0 + (c0 == first);
       }
-      __syncthreads();
-      if (plan[6]) {
-        __threadfence();
-        attend_join<D>(p, first, last, rows, out_row, join);
+      while (attend_arrive(ticket, members, plan + 6)) {
+        const bool final = n <= 32 || step == 32;
+        attend_join<D>(p.parts, first, c0, members, step, rows, final, out, lse, join);
+        if (final) break;
+        c0 = first;
+        members = (n + 31) / 32;
+        step = 32;
+        ticket = p.tickets + first;
       }
     }
     __syncthreads();
