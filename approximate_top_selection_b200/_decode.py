@@ -15,9 +15,36 @@ from ._binding import (TOPK_CACHE_BF16, TOPK_CACHE_E4M3, TopkCache, _check, _cud
 
 _E4M3, _BF16, _F32, _I32, _I64 = torch.float8_e4m3fn, torch.bfloat16, torch.float32, torch.int32, torch.int64
 
-# A step of a few microseconds on the GPU leaves the host as little time, so a
-# call first asks in a few cheap tests whether everything is as usual (get_device
-# is -1 on the CPU) and looks for what is wrong, test by test, only if not.
+# A step of a few microseconds on the GPU leaves the host as little time.  So a
+# call with nothing given but its inputs goes to the extension module
+# _decode_calls, which makes it if everything is as usual; otherwise, and where
+# that finds something unusual, the call is checked and made here (get_device is
+# -1 on the CPU).
+_calls = None
+
+
+def _usual():
+    """The extension module, bound to the CUDA library."""
+    global _calls
+    if _calls is None:
+        lib = load_library()
+        try:
+            from . import _decode_calls as calls
+        except ImportError as e:
+            raise ImportError("_decode_calls.so is missing or does not fit this torch: build it with "
+                              "`python -m approximate_top_selection_b200.build`") from e
+        calls.bind(*(ctypes.cast(f, ctypes.c_void_p).value for f in (
+            lib.paged_attention, lib.paged_attention_workspace_bytes, lib.cache_write, lib.cache_read, lib.topk_beam,
+            lib.topk_beam_bf16, lib.topk_beam_workspace_bytes, lib.beam_reorder)))
+        _calls = calls
+    return _calls
+
+
+def _made(result, where: str):
+    """The outputs of a call that _decode_calls made, or the error it met."""
+    if type(result) is int:
+        _check(result, where)
+    return result
 
 
 def _cuda_strided(t: torch.Tensor, name: str, dtype, dims: int) -> None:
@@ -197,6 +224,11 @@ def paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
     Returns out [batch, heads, d] bfloat16, or (out, lse [batch, heads]
     float32).  A head with nothing to attend to gives zeros and -inf.
     """
+    if stream is None and out is None and out_lse is None and workspace is None:
+        made = (_calls or _usual()).paged_attention(q, k_cache, v_cache, block_table, seq_lens, k_scale, v_scale, positions,
+                                                    scale, return_lse)
+        if made is not None:
+            return _made(made, "paged_attention")
     dev = _device_of(q, "q")
     shape, strides = q.shape, q.stride()
     if q.dtype is not _BF16 or len(shape) != 3 or strides[2] != 1:
@@ -248,6 +280,11 @@ def cache_write(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cache
     must be distinct.  Caches and scales as in paged_attention; an e4m3 row
     gets the smallest power-of-two scale that holds it.
     """
+    if stream is None:
+        made = (_calls or _usual()).cache_write(k, v, k_cache, v_cache, slots, k_scale, v_scale)
+        if made is not None:
+            _made(made, "cache_write")
+            return
     dev = _device_of(k, "k")
     kc, vc, cache_shape = _two_caches(k_cache, v_cache, k_scale, v_scale, dev)
     shape, ks = k.shape, k.stride()
@@ -285,6 +322,10 @@ def cache_read(cache: torch.Tensor, block_table: torch.Tensor, seq_lens: torch.T
     Rows behind a sequence's end are zeros.  `out.view(-1, n, d)` is the key
     matrix per row that score_topk and score_rerank take.
     """
+    if stream is None and out is None:
+        made = (_calls or _usual()).cache_read(cache, block_table, seq_lens, n, scale)
+        if made is not None:
+            return _made(made, "cache_read")
     dev = _device_of(cache, "cache")
     c, (_, kv_heads, _, d) = _cache(cache, scale, "cache", dev)
     batch = seq_lens.numel() if isinstance(seq_lens, torch.Tensor) else 0
@@ -317,6 +358,10 @@ def topk_beam(logits: torch.Tensor, beam_scores: torch.Tensor, k: int, *, out_sc
     parents int32, tokens int32), each [batch, k], best first, padded with
     -inf, -1, -1.
     """
+    if stream is None and out_scores is None and out_parent is None and out_token is None and workspace is None:
+        made = (_calls or _usual()).topk_beam(logits, beam_scores, k)
+        if made is not None:
+            return _made(made, "topk_beam")
     dev = _device_of(logits, "logits")
     bf16 = logits.dtype is _BF16
     try:
@@ -360,6 +405,11 @@ def beam_reorder(states, parents: torch.Tensor, *, out=None, stream=None):
     that is -1.  `out` (of the same form) must not overlap the states.
     """
     one = isinstance(states, torch.Tensor)
+    if stream is None and out is None:
+        made = (_calls or _usual()).beam_reorder([states] if one else states, parents)
+        if made is not None:
+            made = _made(made, "beam_reorder")
+            return made[0] if one else made
     src = [states] if one else list(states)
     dev = _device_of(parents, "parents")
     if parents.dtype is not _I32 or not parents.is_contiguous():
