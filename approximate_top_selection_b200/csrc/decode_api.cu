@@ -114,9 +114,9 @@ template <int D, bool kE4m3>
 int launch_write(const WriteArgs& a, const DeviceInfo& dev, cudaStream_t st) {
   int rc = prepare_kernel(cache_write_kernel<D, kE4m3>);
   if (rc) return rc;
-  const int64_t rows = a.tokens * a.cache[0].kv_heads * 2;
-  const int64_t per = 256 / (D / 16);
-  const int64_t grid = std::min((rows + per - 1) / per, static_cast<int64_t>(dev.sms) * 8);
+  (void)dev;
+  const int64_t rows = (a.tokens + kWriteBlock - 1) / kWriteBlock * kWriteBlock * 2 * a.cache[0].kv_heads;
+  const int64_t grid = std::min((rows + write_rows_per_cta<D>() - 1) / write_rows_per_cta<D>(), kMaxGridX);
   return launch_pdl(cache_write_kernel<D, kE4m3>, dim3(static_cast<unsigned>(grid)), dim3(256), 0, st, a);
 }
 

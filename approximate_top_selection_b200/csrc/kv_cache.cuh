@@ -106,44 +106,45 @@ struct WriteArgs {
   int64_t tokens;
 };
 
-// D / 16 lanes per row, 16 values a lane; kWriteRows rows of a lane group in
-// flight.  Rows (token, k or v, head) are numbered in that order, so that
-// neighbouring groups read neighbouring memory; a group's next row is found by
-// addition (a 64-bit division per row costs more than the row's bytes).
-// Bound by memory: every value is read once (2 bytes) and written once.
-constexpr int kWriteRows = 4;
+// D / 16 lanes per row, 16 values a lane, kWriteRows rows of a lane group in
+// flight; a CTA takes 256 / (D / 16) * kWriteRows rows.  Rows are numbered by
+// blocks of 16 tokens, in a block by (k or v, head), then by token: the rows of
+// a warp are successive tokens of one head, which in a prompt are neighbours
+// in the cache, and so are their scales.  Bound by memory: every value is read
+// once (2 bytes) and written once.
+constexpr int kWriteRows = 2;
+constexpr int kWriteBlock = 16;
+
+template <int D>
+__host__ __device__ constexpr int write_rows_per_cta() {
+  return 256 / (D / 16) * kWriteRows;
+}
 
 template <int D, bool kE4m3>
-__global__ void __launch_bounds__(256) cache_write_kernel(WriteArgs p) {
-  constexpr int L = D / 16;
+__global__ void __launch_bounds__(256, 4) cache_write_kernel(WriteArgs p) {
+  constexpr int L = D / 16, kGroups = 256 / L;
   pdl_wait_then_release();
   const int heads = p.cache[0].kv_heads;
-  const int lines = 2 * heads;  // rows of a token
-  const int64_t rows = p.tokens * lines;
-  const int64_t groups = static_cast<int64_t>(gridDim.x) * (256 / L);
-  const int64_t token_step = groups / lines;
-  const int line_step = static_cast<int>(groups - token_step * lines);
+  const int64_t block_rows = 2 * static_cast<int64_t>(heads) * kWriteBlock;
+  const int64_t rows = (p.tokens + kWriteBlock - 1) / kWriteBlock * block_rows;
   const int gl = threadIdx.x % L;
   const unsigned mask = ((1u << L) - 1u) << (threadIdx.x % 32 / L * L);
-  int64_t r = static_cast<int64_t>(blockIdx.x) * (256 / L) + threadIdx.x / L;
-  int64_t t = r / lines;
-  int line = static_cast<int>(r - t * lines);
-  while (r < rows) {
+  for (int64_t r0 = static_cast<int64_t>(blockIdx.x) * write_rows_per_cta<D>(); r0 < rows;
+       r0 += static_cast<int64_t>(gridDim.x) * write_rows_per_cta<D>()) {
+    const int64_t block0 = r0 / block_rows, in_block = r0 - block0 * block_rows;
     int64_t slot[kWriteRows];
     int64_t tok[kWriteRows];
     int ln[kWriteRows];
 #pragma unroll
     for (int i = 0; i < kWriteRows; ++i) {
-      tok[i] = t;
-      ln[i] = line;
-      slot[i] = r < rows ? __ldg(p.slots + t) : -1;
-      r += groups;
-      t += token_step;
-      line += line_step;
-      if (line >= lines) {
-        line -= lines;
-        ++t;
+      int64_t j = in_block + i * kGroups + threadIdx.x / L, block = block0;
+      while (j >= block_rows) {  // at most a few blocks on: a CTA has 128 rows, a block 32 or more
+        j -= block_rows;
+        ++block;
       }
+      ln[i] = static_cast<int>(j / kWriteBlock);
+      tok[i] = block * kWriteBlock + j % kWriteBlock;
+      slot[i] = tok[i] < p.tokens ? __ldg(p.slots + tok[i]) : -1;
     }
     uint4 x[kWriteRows][2];
 #pragma unroll
@@ -214,7 +215,7 @@ struct ReadArgs {
 // head: D / 16 lanes per row, 16 values a lane, kReadRows rows of a lane group
 // in flight.  Rows past a sequence's end (and rows whose page does not exist)
 // are zero.  Bound by memory: the cached row read once, 2 bytes a value written.
-constexpr int kReadRows = 4;
+constexpr int kReadRows = 2;
 
 template <int D>
 __host__ __device__ constexpr int read_rows_per_cta() {
@@ -222,7 +223,7 @@ __host__ __device__ constexpr int read_rows_per_cta() {
 }
 
 template <int D, bool kE4m3>
-__global__ void __launch_bounds__(256) cache_read_kernel(ReadArgs p) {
+__global__ void __launch_bounds__(256, 8) cache_read_kernel(ReadArgs p) {
   constexpr int L = D / 16, kGroups = 256 / L;
   pdl_wait_then_release();
   const CacheView& c = p.cache;
