@@ -237,7 +237,9 @@ int paged_attention(const uint16_t* q, int64_t q_stride, int64_t batch, int head
   a.tickets = static_cast<uint32_t*>(workspace);
   a.parts = reinterpret_cast<float*>(static_cast<unsigned char*>(workspace) + kTicketBytes);
   a.same_strides = a.k.page_stride == a.v.page_stride && a.k.head_stride == a.v.head_stride &&
-                   a.k.token_stride == a.v.token_stride;
+                   a.k.token_stride == a.v.token_stride &&
+                   (!a.k.scale || (a.k.s_page_stride == a.v.s_page_stride && a.k.s_head_stride == a.v.s_head_stride &&
+                                   a.k.s_token_stride == a.v.s_token_stride));
   // t / page_size for t < 2^31 by a multiplication: 2^shift / page_size rounded up, shift = 31 + ceil(log2 page_size)
   a.page_shift = 31;
   while ((1LL << (a.page_shift - 31)) < k_cache->page_size) ++a.page_shift;

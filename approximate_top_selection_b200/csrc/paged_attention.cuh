@@ -44,7 +44,7 @@ struct AttendArgs {
   int row_tiles;      // groups of 16 query heads per list
   uint32_t page_magic, page_shift;  // t / page_size = (t * page_magic) >> page_shift for 0 <= t < 2^31
   bool grouped;       // no positions, 16 | page_size (16 tokens from a multiple of 16 on share a page), same strides
-  bool same_strides;  // k and v have equal strides
+  bool same_strides;  // k and v, and their scales, have equal strides
   float scale_log2;   // softmax scale * log2(e)
   uint16_t* out;      // [batch][heads][d] bf16
   float* lse;         // null, or [batch][heads]
@@ -179,9 +179,10 @@ __device__ __forceinline__ float column_sum(float x) {
 __device__ __forceinline__ float finite_or_zero(float m) { return m == __int_as_float(0xff800000) ? 0.0f : m; }
 
 // ---------------------------------------------------------------- work line
-// Where a CTA stands on the line of granules.
+// Where a CTA stands on the line of granules: a unit is a sequence, a list of
+// query heads and 16 of the list's heads.
 struct AttendCursor {
-  int b, unit;   // sequence, unit of it (list and group of 16 heads)
+  int b, list, tile;  // sequence, list, group of 16 heads
   int at;        // granule within the unit
   int count;     // tokens or list slots of the unit
   int granules;  // of the unit
@@ -198,21 +199,38 @@ __device__ __forceinline__ void cursor_enter(const AttendArgs& p, AttendCursor& 
   u.granules = granules_of<kGranule>(u.count);
 }
 
-// To the next granule; past the last one `b` is tab.batch and nothing may be read.
+// To the next granule; past the last one `b` is tab.batch and nothing may be
+// read.  Returns whether another unit begins.
 template <int kGranule>
-__device__ __forceinline__ void cursor_next(const AttendArgs& p, AttendCursor& u) {
-  if (++u.at < u.granules) return;
+__device__ __forceinline__ bool cursor_next(const AttendArgs& p, AttendCursor& u) {
+  if (++u.at < u.granules) return false;
   u.at = 0;
-  if (++u.unit < p.lists * p.row_tiles) return;
-  u.unit = 0;
+  if (++u.tile < p.row_tiles) return true;
+  u.tile = 0;
+  if (++u.list < p.lists) return true;
+  u.list = 0;
   do {
     if (++u.b >= p.tab.batch) {
       u.granules = 0;
       u.count = 0;
-      return;
+      return true;
     }
     cursor_enter<kGranule>(p, u);
   } while (u.granules == 0);
+  return true;
+}
+
+// Share c of `total` granules among `ctas`; in 32 bits where that is enough
+// (a 64-bit division takes a few hundred cycles of a call's start).
+__device__ __forceinline__ int64_t attend_share(int64_t total, int ctas, int c) {
+  if (total < (1 << 21)) return static_cast<uint32_t>(total) * static_cast<uint32_t>(c) / static_cast<uint32_t>(ctas);
+  return part_start(total, ctas, c, 1, total);
+}
+__device__ __forceinline__ int attend_owner(int64_t granule, int64_t total, int ctas) {
+  if (total < (1 << 21))
+    return static_cast<int>((static_cast<uint32_t>(granule + 1) * static_cast<uint32_t>(ctas) - 1) /
+                            static_cast<uint32_t>(total));
+  return part_of(granule, total, ctas, 1);
 }
 
 // ---------------------------------------------------------------- one warp's state
@@ -709,17 +727,18 @@ __global__ void __launch_bounds__(kAttendThreads, (AttendShape<D, kE4m3, NT>::kC
   AttendCursor cur;
   auto share = [&]() {
     ctas = static_cast<int>(min(static_cast<int64_t>(gridDim.x), total));
-    g0 = part_start(total, max(ctas, 1), min(static_cast<int>(blockIdx.x), ctas), 1, total);
-    g1 = part_start(total, max(ctas, 1), min(static_cast<int>(blockIdx.x) + 1, ctas), 1, total);
+    g0 = static_cast<int>(blockIdx.x) < ctas ? attend_share(total, ctas, blockIdx.x) : total;
+    g1 = static_cast<int>(blockIdx.x) < ctas ? attend_share(total, ctas, blockIdx.x + 1) : total;
   };
   if (p.positions) {
     cur.b = 0;
     cursor_enter<S::kGranule>(p, cur);
     total = static_cast<int64_t>(p.tab.batch) * units * cur.granules;
     share();
+    if (g0 >= g1) return;
     const int64_t u = g0 / cur.granules;
     cur.b = static_cast<int>(u / units);
-    cur.unit = static_cast<int>(u - static_cast<int64_t>(cur.b) * units);
+    cur.list = static_cast<int>(u - static_cast<int64_t>(cur.b) * units);
     cur.at = static_cast<int>(g0 - u * cur.granules);
   } else {
     // Running sums of the sequences' granules: a stretch of sequences per thread.
@@ -754,14 +773,14 @@ __global__ void __launch_bounds__(kAttendThreads, (AttendShape<D, kE4m3, NT>::kC
       plan[5] = g0 - before;
     }
     __syncthreads();
-    if (g0 < g1) {
-      cur.b = static_cast<int>(plan[4]);
-      cursor_enter<S::kGranule>(p, cur);
-      cur.unit = static_cast<int>(plan[5] / cur.granules);
-      cur.at = static_cast<int>(plan[5] - static_cast<int64_t>(cur.unit) * cur.granules);
-    }
+    if (g0 >= g1) return;
+    cur.b = static_cast<int>(plan[4]);
+    cursor_enter<S::kGranule>(p, cur);
+    cur.list = static_cast<int>(plan[5] / cur.granules);
+    cur.at = static_cast<int>(plan[5] - static_cast<int64_t>(cur.list) * cur.granules);
   }
-  if (g0 >= g1) return;
+  cur.tile = cur.list % p.row_tiles;
+  cur.list /= p.row_tiles;
 
   // The three steps of a tile.  A lane of index < kKeys has a key.  Where a
   // tile lies: its sequence, its key-value head, the sequence's length and the
@@ -769,58 +788,58 @@ __global__ void __launch_bounds__(kAttendThreads, (AttendShape<D, kE4m3, NT>::kC
   AttendCursor ahead = cur;
   int64_t ahead_left = g1 - g0;
   const int kv_per = p.lists / p.k.kv_heads;
+  int ahead_kv = cur.list / kv_per;
+  int ahead_len = p.positions ? seq_length(p.tab, cur.b) : cur.count;
   const uint32_t tokens_addr = smem_addr(tokens), pages_addr = smem_addr(pages);
   auto fetch_tokens = [&](int slot) {
     int4 place = make_int4(0, 0, 0, -1);
     if (ahead_left > 0) {
       const uint32_t i0 = (static_cast<uint32_t>(ahead.at) * kAttendWarps + warp) * S::kKeys;
-      const int list = ahead.unit / p.row_tiles;
-      const int len = p.positions ? seq_length(p.tab, ahead.b) : ahead.count;
-      place = make_int4(ahead.b, list / kv_per, len, static_cast<int>(min(i0, 0x7fffffffu)));
+      place = make_int4(ahead.b, ahead_kv, ahead_len, static_cast<int>(min(i0, 0x7fffffffu)));
       if (p.positions && lane < S::kKeys) {
         const bool on = i0 + lane < static_cast<uint32_t>(ahead.count);
         copy4(tokens_addr + (slot * S::kKeys + lane) * 4,
-              p.positions + (static_cast<int64_t>(ahead.b) * p.lists + list) * p.c + (on ? i0 + lane : 0), on);
+              p.positions + (static_cast<int64_t>(ahead.b) * p.lists + ahead.list) * p.c + (on ? i0 + lane : 0), on);
       }
       --ahead_left;
-      cursor_next<S::kGranule>(p, ahead);
+      if (cursor_next<S::kGranule>(p, ahead) && ahead_left > 0) {
+        ahead_kv = ahead.list / kv_per;
+        ahead_len = p.positions ? seq_length(p.tab, ahead.b) : ahead.count;
+      }
     }
     if (lane == 0) places[slot] = place;
   };
-  // The lane's token, or -1 (a list's slots behind its end were filled with
-  // zeros by the copy, so they are told by their index).
-  auto token_of = [&](int slot, const int4& place) {
-    if (place.w < 0 || lane >= S::kKeys) return -1;
-    const uint32_t i = static_cast<uint32_t>(place.w) + lane;
-    if (!p.positions) return i < static_cast<uint32_t>(place.z) ? static_cast<int>(i) : -1;
-    return i < static_cast<uint32_t>(p.c) ? tokens[slot * S::kKeys + lane] : -1;
-  };
+  // The lane's token turns into its page, asked for here, and its offset there
+  // (-1: no token).  A list's slots behind its end are told by their index.
   auto fetch_pages = [&](int slot) {
     const int4 place = places[slot];
-    const int tok = token_of(slot, place);
-    const bool on = tok >= 0 && tok < place.z;
-    if (tok >= p.tab.capacity) atomicOr(&g_device_status, kDevBadIndex);
-    const int64_t at = on ? static_cast<int64_t>((static_cast<uint64_t>(tok) * p.page_magic) >> p.page_shift) : 0;
-    if (lane < S::kKeys) copy4(pages_addr + (slot * S::kKeys + lane) * 4, p.tab.table + place.x * p.tab.stride + at, on);
+    if (lane < S::kKeys) {
+      const uint32_t i = static_cast<uint32_t>(place.w) + lane;
+      int tok = -1;
+      if (place.w >= 0 && i < static_cast<uint32_t>(p.positions ? p.c : place.z))
+        tok = p.positions ? tokens[slot * S::kKeys + lane] : static_cast<int>(i);
+      const bool on = tok >= 0 && tok < place.z;
+      if (tok >= p.tab.capacity) atomicOr(&g_device_status, kDevBadIndex);
+      const int at = on ? static_cast<int>((static_cast<uint64_t>(tok) * p.page_magic) >> p.page_shift) : 0;
+      copy4(pages_addr + (slot * S::kKeys + lane) * 4, p.tab.table + place.x * p.tab.stride + at, on);
+      tokens[slot * S::kKeys + lane] = on ? tok - at * p.k.page_size : -1;
+    }
   };
   auto fetch_rows = [&](int stage, int slot) {
-    const int4 place = places[slot];
-    const int tok = token_of(slot, place);
-    bool live = tok >= 0 && tok < place.z;
+    const int page_kv = places[slot].y;
+    int o = lane < S::kKeys ? tokens[slot * S::kKeys + lane] : -1;
+    bool live = o >= 0;
     int64_t pg = 0;
-    int o = 0;
     if (live) {
       pg = pages[slot * S::kKeys + lane];
-      o = tok - static_cast<int>((static_cast<uint64_t>(tok) * p.page_magic) >> p.page_shift) * p.k.page_size;
       if (pg < 0 || pg >= p.k.pages) {
         atomicOr(&g_device_status, kDevBadIndex);
         live = false;
         pg = 0;
-        o = 0;
       }
     }
+    if (!live) o = 0;
     const uint32_t valid = __ballot_sync(0xffffffffu, live);
-    const int page_kv = place.y;
     const int64_t ko = pg * p.k.page_stride + page_kv * p.k.head_stride + o * p.k.token_stride;
     int64_t vo = ko;
     if (!p.same_strides) vo = pg * p.v.page_stride + page_kv * p.v.head_stride + o * p.v.token_stride;
@@ -878,9 +897,11 @@ __global__ void __launch_bounds__(kAttendThreads, (AttendShape<D, kE4m3, NT>::kC
       if constexpr (kE4m3) {
         if (lane < S::kKeys) {
           const uint32_t st = vt + S::kTileBytes + lane * 4;
-          copy4(st, p.k.scale + (pg * p.k.s_page_stride + page_kv * p.k.s_head_stride + o * p.k.s_token_stride), live);
-          copy4(st + S::kKeys * 4,
-                p.v.scale + (pg * p.v.s_page_stride + page_kv * p.v.s_head_stride + o * p.v.s_token_stride), live);
+          const int64_t ks = pg * p.k.s_page_stride + page_kv * p.k.s_head_stride + o * p.k.s_token_stride;
+          int64_t vs = ks;
+          if (!p.same_strides) vs = pg * p.v.s_page_stride + page_kv * p.v.s_head_stride + o * p.v.s_token_stride;
+          copy4(st, p.k.scale + ks, live);
+          copy4(st + S::kKeys * 4, p.v.scale + vs, live);
         }
       }
     }
@@ -927,9 +948,8 @@ __global__ void __launch_bounds__(kAttendThreads, (AttendShape<D, kE4m3, NT>::kC
   int stage = 0;
 #pragma unroll 1
   for (int64_t g = g0; g < g1; ++g) {
-    const int list = cur.unit / p.row_tiles, mt = cur.unit - list * p.row_tiles;
-    const int rows = min(16, group - mt * 16);
-    const int head = list * group + mt * 16;
+    const int rows = min(16, group - cur.tile * 16);
+    const int head = cur.list * group + cur.tile * 16;
     if (fresh) {
       if constexpr (S::kQShared) __syncthreads();
       w.load_q(p, p.q + cur.b * p.q_stride + static_cast<int64_t>(head) * D, rows, shared_q, warp);
@@ -1039,8 +1059,8 @@ __global__ void __launch_bounds__(kAttendThreads, (AttendShape<D, kE4m3, NT>::kC
       // Up to 32 parts are joined at once; more by groups of 32, and then the
       // groups (one CTA reading hundreds of parts would take longer than the
       // cache did).
-      const int first = part_of(unit_first, total, ctas, 1);
-      const int last = part_of(unit_first + cur.granules - 1, total, ctas, 1);
+      const int first = attend_owner(unit_first, total, ctas);
+      const int last = attend_owner(unit_first + cur.granules - 1, total, ctas);
       const int n = last - first + 1, me = static_cast<int>(blockIdx.x) - first;
       uint16_t* out = p.out + out_row * D;
       float* lse = p.lse ? p.lse + out_row : nullptr;
