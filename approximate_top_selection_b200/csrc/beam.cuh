@@ -105,14 +105,18 @@ __device__ __forceinline__ uint32_t beam_bound(uint32_t mine, int k, uint32_t* w
   if ((threadIdx.x & 31) == 0) warp_keys[threadIdx.x >> 5] = last;
   __syncthreads();
   // k <= 8: the k-th largest of the eight warps' maxima; else the smallest.
-  const int want = min(k, kWarps);
-  uint32_t bound = 0;
+  uint32_t bound = warp_keys[0];
+  if (k >= kWarps) {
+#pragma unroll
+    for (int w = 1; w < kWarps; ++w) bound = min(bound, warp_keys[w]);
+    return bound;
+  }
 #pragma unroll
   for (int w = 0; w < kWarps; ++w) {
     int above = 0;
 #pragma unroll
     for (int v = 0; v < kWarps; ++v) above += warp_keys[v] > warp_keys[w] || (warp_keys[v] == warp_keys[w] && v < w);
-    if (above == want - 1) bound = warp_keys[w];
+    if (above == k - 1) bound = warp_keys[w];
   }
   return bound;
 }
@@ -138,7 +142,7 @@ struct BeamShared {
   double off[kMaxBeams];
   double part[kBeamThreads / 32];
   Cont best[kBeamThreads / 32];
-  uint32_t warp_keys[kBeamThreads / 32];
+  uint32_t warp_keys[kBeamThreads / 32], warp_tops[kBeamThreads / 32];
   int count, total, last;
 };
 
@@ -302,57 +306,82 @@ __device__ __forceinline__ void beam_finish(const BeamArgs& p, BeamShared& sh, i
   const float ninf = __int_as_float(0xff800000);
   const BeamSum* sums = p.sums + local * p.beams * p.pieces;
   const uint64_t* lists = p.lists + local * p.beams * p.pieces * p.k;
+  const int total = p.beams * p.pieces * p.k, per_beam = p.k * p.pieces;
+  // The first candidates of every thread stay in registers; their loads are in
+  // flight with those of the sums.
+  constexpr int kHeld = 8;
+  uint64_t held[kHeld];
+#pragma unroll
+  for (int i = 0; i < kHeld; ++i) {
+    const int c = tid + i * kBeamThreads;
+    held[i] = c < total ? __ldcg(lists + c) : 0ull;
+  }
   for (int i = warp; i < p.beams; i += kBeamThreads / 32) {
     uint32_t top = 0;
-    for (int j = lane; j < p.pieces; j += 32) top = max(top, __ldcg(&sums[i * p.pieces + j].top));
-    top = __reduce_max_sync(0xffffffffu, top);
-    const bool bad = top >= 0xff800000u;  // +inf or NaN
-    const double m = top ? static_cast<double>(key_value(top)) : 0.0;
     double sum = 0.0;
-    if (top && !bad)
-      for (int j = lane; j < p.pieces; j += 32) {
-        const uint32_t t = __ldcg(&sums[i * p.pieces + j].top);
-        const double x = __ldcg(&sums[i * p.pieces + j].sum);
+    const float score = __ldg(p.scores + b * p.beams + i);
+    for (int j0 = 0; j0 < p.pieces; j0 += 32) {  // joined as maxima and sums are
+      uint32_t t = 0;
+      double x = 0.0;
+      if (j0 + lane < p.pieces) {
+        const uint4 raw = __ldcg(reinterpret_cast<const uint4*>(sums + i * p.pieces + j0 + lane));
+        t = raw.z;
+        x = __hiloint2double(static_cast<int>(raw.y), static_cast<int>(raw.x));
+      }
+      const uint32_t now = max(top, __reduce_max_sync(0xffffffffu, t));
+      if (now < 0xff800000u) {
+        const double m = now ? static_cast<double>(key_value(now)) : 0.0;
+        if (top && top != now) sum *= exp(static_cast<double>(key_value(top)) - m);
         if (t) sum += x * exp(static_cast<double>(key_value(t)) - m);
       }
+      top = now;
+    }
+    const bool bad = top >= 0xff800000u;  // +inf or NaN
 #pragma unroll
     for (int x = 16; x; x >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
     if (lane == 0)
       sh.off[i] = bad ? __longlong_as_double(0x7ff8000000000000ll)
-                      : static_cast<double>(__ldg(p.scores + b * p.beams + i)) - (m + log(sum));
+                      : static_cast<double>(score) - ((top ? static_cast<double>(key_value(top)) : 0.0) + log(sum));
   }
   if (tid == 0) sh.count = 0;
   __syncthreads();
   // Bound and gather on the values rounded down to float (the order is kept,
   // equal ones stay candidates).
-  const int total = p.beams * p.pieces * p.k;
-  auto value = [&](int c, uint64_t e) {
-    return sh.off[c / (p.k * p.pieces)] + static_cast<double>(key_value(packed_key(e)));
-  };
+  auto value = [&](int c, uint64_t e) { return sh.off[c / per_beam] + static_cast<double>(key_value(packed_key(e))); };
   auto low_key = [&](double v) { return order_key(__double2float_rd(v)); };
   uint32_t mine = 0;
-  for (int c = tid; c < total; c += kBeamThreads) {
+#pragma unroll
+  for (int i = 0; i < kHeld; ++i)
+    if (held[i]) mine = max(mine, low_key(value(tid + i * kBeamThreads, held[i])));
+  for (int c = tid + kHeld * kBeamThreads; c < total; c += kBeamThreads) {
     const uint64_t e = __ldcg(lists + c);
     if (e) mine = max(mine, low_key(value(c, e)));
   }
-  // The k-th largest of the threads' maxima, to 20 bits: beams differ in score,
+  // The k-th largest of the threads' maxima, to 16 bits: beams differ in score,
   // so the bound of the weakest warp would let most candidates through.
   uint32_t bound = 0;
-  for (int bit = 31; bit >= 12; --bit) {
+  for (int bit = 31; bit >= 16; --bit) {
     const uint32_t trial = bound | (1u << bit);
     if (__syncthreads_count(mine >= trial) >= p.k) bound = trial;
   }
   bound = max(bound, 1u);
-  for (int c = tid; c < total; c += kBeamThreads) {
-    const uint64_t e = __ldcg(lists + c);
-    if (!e) continue;
+  auto gather = [&](int c, uint64_t e) {
     const double v = value(c, e);
-    if (low_key(v) < bound) continue;
+    if (low_key(v) < bound) return;
     const int at = atomicAdd(&sh.count, 1);
-    if (at >= kBeamCap) continue;
+    if (at >= kBeamCap) return;
     sh.cont.value[at] = order_key64(v);
-    sh.cont.rest[at] = (static_cast<uint64_t>(~static_cast<uint32_t>(c / (p.k * p.pieces))) << 32) | packed_key(e);
+    sh.cont.rest[at] = (static_cast<uint64_t>(~static_cast<uint32_t>(c / per_beam)) << 32) | packed_key(e);
     sh.cont.token[at] = packed_idx(e);
+  };
+  if (mine >= bound) {
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i)
+      if (held[i]) gather(tid + i * kBeamThreads, held[i]);
+    for (int c = tid + kHeld * kBeamThreads; c < total; c += kBeamThreads) {
+      const uint64_t e = __ldcg(lists + c);
+      if (e) gather(c, e);
+    }
   }
   __syncthreads();
   const int m = sh.count;
@@ -380,7 +409,7 @@ __device__ __forceinline__ void beam_finish(const BeamArgs& p, BeamShared& sh, i
         const uint64_t e = __ldcg(lists + c);
         if (!e) continue;
         const Cont x = {order_key64(value(c, e)),
-                        (static_cast<uint64_t>(~static_cast<uint32_t>(c / (p.k * p.pieces))) << 32) | packed_key(e),
+                        (static_cast<uint64_t>(~static_cast<uint32_t>(c / per_beam)) << 32) | packed_key(e),
                         packed_idx(e)};
         if ((done == 0 || ranks_above(last, x)) && ranks_above(x, top)) top = x;
       }
@@ -443,15 +472,12 @@ __global__ void __launch_bounds__(kBeamThreads, BC) topk_beam_kernel(BeamArgs p)
       top = fmax_nan(top, pc.largest(y));
     }
     const uint32_t mine = beam_key(top);
-    const uint32_t bound = max(beam_bound(mine, p.k, sh.warp_keys), 1u);
-    // the piece's maximum
     const uint32_t warp_top = __reduce_max_sync(0xffffffffu, mine);
-    __syncthreads();
-    if (lane == 0) sh.warp_keys[warp] = warp_top;
-    __syncthreads();
-    uint32_t key_top = 0;
+    if (lane == 0) sh.warp_tops[warp] = warp_top;
+    const uint32_t bound = max(beam_bound(mine, p.k, sh.warp_keys), 1u);
+    uint32_t key_top = 0;  // the piece's maximum
 #pragma unroll
-    for (int w = 0; w < kBeamThreads / 32; ++w) key_top = max(key_top, sh.warp_keys[w]);
+    for (int w = 0; w < kBeamThreads / 32; ++w) key_top = max(key_top, sh.warp_tops[w]);
     // The sum of 2^(x L - M), M = m L rounded, L = log2 e rounded: one fused
     // multiply-add and one exponential a logit.  M's rounding is taken out
     // exactly at the end (M - m L is known in 64 bits); L's moves the exponent
@@ -474,7 +500,7 @@ __global__ void __launch_bounds__(kBeamThreads, BC) topk_beam_kernel(BeamArgs p)
       }
     } else if (key_top) {
       const float ml = m * kLog2e;
-      fix = static_cast<double>(ml) - static_cast<double>(m) * static_cast<double>(kLog2e);
+      if (tid == 0) fix = static_cast<double>(ml) - static_cast<double>(m) * static_cast<double>(kLog2e);
 #pragma unroll
       for (int v = 0; v < kBeamVectors; ++v) {
 #pragma unroll
@@ -526,16 +552,16 @@ __global__ void __launch_bounds__(kBeamThreads, BC) topk_beam_kernel(BeamArgs p)
       *sum_out = BeamSum{t * exp2(fix), key_top};
     }
   }
-  __threadfence();
   __syncthreads();
   if (tid == 0) {
     const uint32_t n = static_cast<uint32_t>(p.beams) * p.pieces - 1;
+    __threadfence();
     sh.last = atomicAdd(p.tickets + local, 1u) == n;
     if (sh.last) p.tickets[local] = 0;
+    __threadfence();
   }
   __syncthreads();
   if (!sh.last) return;
-  __threadfence();
   beam_finish(p, sh, local);
 }
 
