@@ -39,28 +39,34 @@ __device__ __forceinline__ bool ranks_above(const Cont& a, const Cont& b) {
   return a.token < b.token;
 }
 
-// Two levels, one launch.  A CTA takes a piece of a beam's row, at most 64 KB
+// Two kernels.  A CTA of the first takes a piece of a beam's row, at most 64 KB
 // that stay in its registers: the piece's maximum, its sum of exponentials and
-// its k largest logits.  The CTA of a sentence that finishes last (an atomic
-// ticket, nobody waits) turns the sums into lse_i and picks the k best of all
-// pieces' lists.  Within a beam the order is the logits', so a piece's list
-// can be cut at k before lse_i is known.
+// its k largest logits.  A CTA of the second, started as the first drains,
+// turns a sentence's sums into lse_i and picks the k best of all pieces' lists.
+// Within a beam the order is the logits', so a piece's list can be cut at k
+// before lse_i is known.  (Leaving the second part to the CTA that finishes a
+// sentence last costs every CTA a fence and an atomic, 1.1 of its 7 us.)
 //
 // The k largest of a piece without sorting it: of the 256 threads' maxima, the
 // j-th largest of each warp (j = ceil(k / 8)) bounds the k-th largest value
-// from below in all; the few elements at or above the smallest of these bounds
-// are gathered while the exponentials are summed, and ranked by counting.
-// Where that leaves more than kBeamCap (equal logits), the bound is bisected,
-// over keys and then over indices.
+// from below in all; the few vectors that reach the smallest of these bounds
+// are set aside while the exponentials are summed, their elements gathered and
+// ranked by counting.  Where that leaves too many (equal logits), the bound is
+// bisected, over keys and then over indices.
 //
 // Bound by reading the logits.  A logit costs one exponential (16 per clock
 // and SM: 4.5e12 a second, against 1.6e12 fp32 or 3.2e12 bf16 logits a second
-// at full bandwidth) and about six other instructions.
-// A piece's largest key (0: nothing) and sum of exp(x - max).
+// at full bandwidth) and about five other instructions.
+// A piece's largest key (0: nothing) and its sum of 2^(x L - r), with L = log2 e
+// rounded to fp32 and r a whole number near max * L (so that sums join by exact
+// powers of two), or of exp(x - max), r = kBeamByMax, where max is beyond 1e6.
 struct __align__(16) BeamSum {
   double sum;
   uint32_t top;
+  int r;
 };
+constexpr int kBeamByMax = -2147483647 - 1;
+constexpr float kBeamLog2e = 1.4426950408889634f;
 
 struct BeamArgs {
   const void* logits;   // [batch][beams][n]
@@ -72,19 +78,14 @@ struct BeamArgs {
   float* out_scores;    // [batch][k]
   int32_t* out_parent;  // [batch][k]
   int32_t* out_token;   // [batch][k]
-  uint32_t* tickets;    // [sentences of the launch], zero between calls
   BeamSum* sums;        // [rows of the launch][pieces]
   uint64_t* lists;      // [rows of the launch][pieces][k]
 };
 
 constexpr int kMaxBeams = 128;
 constexpr int kBeamCap = 512;       // gathered candidates; more than the largest k
-#ifndef BV
-#define BV 16
-#define BC 2
-#endif
-constexpr int kBeamVectors = BV;    // 16-byte vectors per thread
-constexpr int kBeamTickets = 4096;  // sentences per launch
+constexpr int kBeamHits = 384;      // vectors that hold them
+constexpr int kBeamVectors = 16;   // 16-byte vectors per thread
 
 // Order key of a candidate logit; 0 for one that gives no continuation.
 __device__ __forceinline__ uint32_t beam_key(float x) {
@@ -139,11 +140,13 @@ struct BeamShared {
       uint32_t token[kBeamCap];
     } cont;
   };
+  uint4 hit[kBeamHits];   // vectors of a piece that reach its bound
+  int hit_at[kBeamHits];  // index of their first element
   double off[kMaxBeams];
   double part[kBeamThreads / 32];
   Cont best[kBeamThreads / 32];
   uint32_t warp_keys[kBeamThreads / 32], warp_tops[kBeamThreads / 32];
-  int count, total, last;
+  int count, hits, total;
 };
 
 __device__ __forceinline__ float exp2_ftz(float x) {
@@ -232,12 +235,6 @@ struct BeamPiece {
     asm("set.ge.u32.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(w), "r"(least));
     return d != 0;
   }
-  static __device__ __forceinline__ float value_at(const uint4& x, int e) {  // e not known when compiling
-    const int i = sizeof(T) == 4 ? e : e >> 1;
-    const uint32_t w = i == 0 ? x.x : i == 1 ? x.y : i == 2 ? x.z : x.w;
-    if constexpr (sizeof(T) == 4) return __uint_as_float(w);
-    return __uint_as_float(e & 1 ? w & 0xffff0000u : w << 16);
-  }
   static __device__ __forceinline__ float value(const uint4& x, int e) {
     const int i = e * static_cast<int>(sizeof(T)) / 4;
     const uint32_t w = i == 0 ? x.x : i == 1 ? x.y : i == 2 ? x.z : x.w;
@@ -299,9 +296,31 @@ __device__ __noinline__ void beam_bisect(BeamShared* shp, const T* row, int64_t 
   __syncthreads();
 }
 
-// The k best continuations of a sentence, from its rows' sums and lists.
-__device__ __forceinline__ void beam_finish(const BeamArgs& p, BeamShared& sh, int64_t local) {
+// Calls use(i, rank) for every i < n with the number of j that above(j, i)
+// holds for: four lanes count a quarter each.
+template <typename Above, typename Use>
+__device__ __forceinline__ void beam_rank(int n, Above&& above, Use&& use) {
+  const int q = threadIdx.x & 3;
+  for (int i0 = 0; i0 < n; i0 += kBeamThreads / 4) {
+    const int i = i0 + static_cast<int>(threadIdx.x >> 2);
+    int r = 0;
+    if (i < n) {
+#pragma unroll 4
+      for (int j = q; j < n; j += 4) r += above(j, i);
+    }
+    r += __shfl_xor_sync(0xffffffffu, r, 1);
+    r += __shfl_xor_sync(0xffffffffu, r, 2);
+    if (i < n && q == 0) use(i, r);
+  }
+}
+
+// The k best continuations of sentence blockIdx.x of the launch, from its rows'
+// sums and lists.
+__global__ void __launch_bounds__(kBeamThreads) beam_finish_kernel(BeamArgs p) {
+  __shared__ BeamShared sh;
+  pdl_wait_then_release();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int64_t local = blockIdx.x;
   const int64_t b = p.first + local;
   const float ninf = __int_as_float(0xff800000);
   const BeamSum* sums = p.sums + local * p.beams * p.pieces;
@@ -319,29 +338,43 @@ __device__ __forceinline__ void beam_finish(const BeamArgs& p, BeamShared& sh, i
   for (int i = warp; i < p.beams; i += kBeamThreads / 32) {
     uint32_t top = 0;
     double sum = 0.0;
+    int r = 0;            // of `sum`: 2^r is its unit
+    bool by_max = false;  // some piece's sum is relative to its maximum
     const float score = __ldg(p.scores + b * p.beams + i);
-    for (int j0 = 0; j0 < p.pieces; j0 += 32) {  // joined as maxima and sums are
-      uint32_t t = 0;
-      double x = 0.0;
-      if (j0 + lane < p.pieces) {
-        const uint4 raw = __ldcg(reinterpret_cast<const uint4*>(sums + i * p.pieces + j0 + lane));
-        t = raw.z;
-        x = __hiloint2double(static_cast<int>(raw.y), static_cast<int>(raw.x));
-      }
-      const uint32_t now = max(top, __reduce_max_sync(0xffffffffu, t));
-      if (now < 0xff800000u) {
-        const double m = now ? static_cast<double>(key_value(now)) : 0.0;
-        if (top && top != now) sum *= exp(static_cast<double>(key_value(top)) - m);
-        if (t) sum += x * exp(static_cast<double>(key_value(t)) - m);
-      }
-      top = now;
+    for (int j0 = 0; j0 < p.pieces; j0 += 32) {
+      uint4 raw = make_uint4(0, 0, 0, 0);
+      if (j0 + lane < p.pieces) raw = __ldcg(reinterpret_cast<const uint4*>(sums + i * p.pieces + j0 + lane));
+      const double x = __hiloint2double(static_cast<int>(raw.y), static_cast<int>(raw.x));
+      const int rj = static_cast<int>(raw.w);
+      top = max(top, __reduce_max_sync(0xffffffffu, raw.z));
+      by_max |= __any_sync(0xffffffffu, raw.z && rj == kBeamByMax);
+      const int now = max(j0 ? r : kBeamByMax, __reduce_max_sync(0xffffffffu, raw.z ? rj : kBeamByMax));
+      // differences beyond 1100 leave nothing of a sum below 2^32
+      if (j0) sum = scalbn(sum, max(r - now, -1100));
+      if (raw.z) sum += scalbn(x, max(rj - now, -1100));
+      r = now;
     }
     const bool bad = top >= 0xff800000u;  // +inf or NaN
+    const double m = top ? static_cast<double>(key_value(top)) : 0.0;
+    constexpr double kLn2 = 0.6931471805599453;
+    if (by_max && !bad) {
+      sum = 0.0;
+      for (int j = lane; j < p.pieces; j += 32) {
+        const uint4 raw = __ldcg(reinterpret_cast<const uint4*>(sums + i * p.pieces + j));
+        const double x = __hiloint2double(static_cast<int>(raw.y), static_cast<int>(raw.x));
+        const int rj = static_cast<int>(raw.w);
+        if (raw.z) sum += x * exp((rj == kBeamByMax ? static_cast<double>(key_value(raw.z)) : rj * kLn2) - m);
+      }
+    }
 #pragma unroll
     for (int x = 16; x; x >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
-    if (lane == 0)
-      sh.off[i] = bad ? __longlong_as_double(0x7ff8000000000000ll)
-                      : static_cast<double>(score) - ((top ? static_cast<double>(key_value(top)) : 0.0) + log(sum));
+    if (lane == 0) {
+      // L (1 + e) = log2 e: the terms' exponents are short by e x, all but
+      // e (x - m) of which is given back here.
+      constexpr double kShort = 1.4426950408889634 / static_cast<double>(kBeamLog2e) - 1.0;
+      const double lse = by_max ? m + log(sum) : r * kLn2 + log(sum) + kShort * m;
+      sh.off[i] = bad ? __longlong_as_double(0x7ff8000000000000ll) : static_cast<double>(score) - lse;
+    }
   }
   if (tid == 0) sh.count = 0;
   __syncthreads();
@@ -393,13 +426,12 @@ __device__ __forceinline__ void beam_finish(const BeamArgs& p, BeamShared& sh, i
   };
   int done = min(m, p.k);
   if (m <= kBeamCap) {
-    for (int i = tid; i < m; i += kBeamThreads) {
-      const Cont mine = {sh.cont.value[i], sh.cont.rest[i], sh.cont.token[i]};
-      int above = 0;
-      for (int j = 0; j < m; ++j)
-        above += ranks_above(Cont{sh.cont.value[j], sh.cont.rest[j], sh.cont.token[j]}, mine);
-      if (above < p.k) write(b * p.k + above, mine);
-    }
+    auto cont = [&](int i) { return Cont{sh.cont.value[i], sh.cont.rest[i], sh.cont.token[i]}; };
+    beam_rank(
+        m, [&](int j, int i) { return ranks_above(cont(j), cont(i)); },
+        [&](int i, int r) {
+          if (r < p.k) write(b * p.k + r, cont(i));
+        });
   } else {
     // Too many near-equal values: one round over the lists per continuation.
     Cont last = {~0ull, ~0ull, 0};
@@ -438,24 +470,25 @@ __device__ __forceinline__ void beam_finish(const BeamArgs& p, BeamShared& sh, i
 
 // Grid: sentence-major, then beam, then piece.
 template <typename T>
-__global__ void __launch_bounds__(kBeamThreads, BC) topk_beam_kernel(BeamArgs p) {
+__global__ void __launch_bounds__(kBeamThreads, 2) topk_beam_kernel(BeamArgs p) {
   constexpr int kPer = BeamPiece<T>::kPer;
   __shared__ BeamShared sh;
   pdl_wait_then_release();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int64_t row = blockIdx.x / p.pieces;  // of the launch
   const int piece = static_cast<int>(blockIdx.x - row * p.pieces);
-  const int64_t local = row / p.beams;
   BeamSum* sum_out = p.sums + blockIdx.x;
   uint64_t* list = p.lists + static_cast<int64_t>(blockIdx.x) * p.k;
   const float ninf = __int_as_float(0xff800000);
-  if (tid == 0) sh.count = 0;
+  if (tid == 0) sh.count = sh.hits = 0;
   if (__ldg(p.scores + p.first * p.beams + row) == ninf) {
-    if (tid == 0) *sum_out = BeamSum{0.0, 0u};
+    if (tid == 0) *sum_out = BeamSum{0.0, 0u, 0};
     for (int i = tid; i < p.k; i += kBeamThreads) list[i] = 0;
   } else {
     const T* row_x = static_cast<const T*>(p.logits) + (p.first * p.beams + row) * p.n;
     const BeamPiece<T> pc(row_x, p.n, piece, p.pieces);
+    // (vectors that no thread of the piece has are passed over)
+    auto any = [&](int v) { return v * kBeamThreads < pc.low + pc.count; };
     uint4 x[kBeamVectors];
 #pragma unroll
     for (int v = 0; v < kBeamVectors; ++v) x[v] = pc.load(v);
@@ -464,13 +497,11 @@ __global__ void __launch_bounds__(kBeamThreads, BC) topk_beam_kernel(BeamArgs p)
     const int64_t edge_at = tid == 0 ? pc.first_ragged() : tid == 32 ? pc.last_ragged() : -1;
     if (edge_at >= 0) edge = pc.load_ragged(edge_at);
     // largest element of the thread (NaN counts as the largest), and the bound
-    float top = pc.largest(edge);
-    {
-      uint4 y = x[0];
+    uint4 y = edge;
 #pragma unroll
-      for (int v = 1; v < kBeamVectors; ++v) y = pc.larger(y, x[v]);
-      top = fmax_nan(top, pc.largest(y));
-    }
+    for (int v = 0; v < kBeamVectors; ++v)
+      if (any(v)) y = pc.larger(y, x[v]);
+    const float top = pc.largest(y);
     const uint32_t mine = beam_key(top);
     const uint32_t warp_top = __reduce_max_sync(0xffffffffu, mine);
     if (lane == 0) sh.warp_tops[warp] = warp_top;
@@ -478,91 +509,71 @@ __global__ void __launch_bounds__(kBeamThreads, BC) topk_beam_kernel(BeamArgs p)
     uint32_t key_top = 0;  // the piece's maximum
 #pragma unroll
     for (int w = 0; w < kBeamThreads / 32; ++w) key_top = max(key_top, sh.warp_tops[w]);
-    // The sum of 2^(x L - M), M = m L rounded, L = log2 e rounded: one fused
-    // multiply-add and one exponential a logit.  M's rounding is taken out
-    // exactly at the end (M - m L is known in 64 bits); L's moves the exponent
-    // of a term by 2^-26 of (x - m) log2 e.
-    constexpr float kLog2e = 1.4426950408889634f;
+    // The sum of 2^(x L - r): one fused multiply-add and one exponential a
+    // logit.  L's rounding moves the exponent of a term by 2^-26 of x log2 e, of
+    // which the part common to all terms is taken out at the end.  Vectors that
+    // reach the bound are set aside, and their elements then looked at by all
+    // threads.
     float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    double fix = 0.0;   // log2 of what the sum is to be multiplied by
-    uint32_t hits = 0;  // vectors with an element at or above the bound
+    int r = 0;
+    bool gathered = false;
     const float m = key_top ? key_value(key_top) : 0.0f;
-    const uint32_t least = pc.bits(bound == 1u ? 0xff7fffffu : __float_as_uint(key_value(bound)));
-    if (key_top >= 0xff800000u) {  // a NaN or +inf: no sum, and every vector is looked at
-      hits = (1u << kBeamVectors) - 1;
-    } else if (fabsf(m) > 1e6f) {  // m L would be off by more than a fraction of 1
-      hits = (1u << kBeamVectors) - 1;
+    if (key_top >= 0xff800000u) {  // a NaN or +inf: no sum
+    } else if (fabsf(m) > 1e6f) {  // x L would be off by more than a fraction of 1
+      r = kBeamByMax;
 #pragma unroll 1
       for (int v = 0; v <= kBeamVectors; ++v) {
-        const uint4 y = v < kBeamVectors ? pc.load(v) : edge;
+        const uint4 z = v < kBeamVectors ? pc.load(v) : edge;
 #pragma unroll
-        for (int e = 0; e < kPer; ++e) sum[e & 3] += exp2_ftz((pc.value(y, e) - m) * kLog2e);
+        for (int e = 0; e < kPer; ++e) sum[e & 3] += exp2_ftz((pc.value(z, e) - m) * kBeamLog2e);
       }
     } else if (key_top) {
-      const float ml = m * kLog2e;
-      if (tid == 0) fix = static_cast<double>(ml) - static_cast<double>(m) * static_cast<double>(kLog2e);
+      gathered = true;
+      const uint32_t least = pc.bits(bound == 1u ? 0xff7fffffu : __float_as_uint(key_value(bound)));
+      const float rf = rintf(m * kBeamLog2e);
+      r = static_cast<int>(rf);
+      auto add = [&](const uint4& z, int64_t i) {
 #pragma unroll
-      for (int v = 0; v < kBeamVectors; ++v) {
+        for (int e = 0; e < kPer; ++e) sum[e & 3] += exp2_ftz(fmaf(pc.value(z, e), kBeamLog2e, -rf));
+        if (pc.reaches(z, least)) {
+          const int at = atomicAdd(&sh.hits, 1);
+          if (at < kBeamHits) {
+            sh.hit[at] = z;
+            sh.hit_at[at] = static_cast<int>(i);
+          }
+        }
+      };
 #pragma unroll
-        for (int e = 0; e < kPer; ++e) sum[e & 3] += exp2_ftz(fmaf(pc.value(x[v], e), kLog2e, -ml));
-        hits |= pc.reaches(x[v], least) ? 1u << v : 0u;
+      for (int v = 0; v < kBeamVectors; ++v)
+        if (any(v)) add(x[v], pc.index(v));
+      if (edge_at >= 0) add(edge, edge_at * kPer - pc.mis);
+      __syncthreads();
+      const int hits = min(sh.hits, kBeamHits);
+      for (int i = tid; i < hits * kPer; i += kBeamThreads) {
+        const uint32_t key = beam_key(logit_value(reinterpret_cast<const T*>(sh.hit)[i]));
+        if (key >= bound) beam_push(sh, key, sh.hit_at[i / kPer] + i % kPer);
       }
-      if (edge_at >= 0)
-#pragma unroll
-        for (int e = 0; e < kPer; ++e) sum[e & 3] += exp2_ftz(fmaf(pc.value(edge, e), kLog2e, -ml));
     }
-    // The hits' elements are read once more (from L2), which keeps this loop small.
-    const float floor_value = bound == 1u ? ninf : key_value(bound);
-    auto gather = [&](const uint4& y, int64_t i) {
-      uint32_t at = 0;
-#pragma unroll
-      for (int e = 0; e < kPer; ++e) at |= !(pc.value(y, e) < floor_value) ? 1u << e : 0u;  // NaN too
-      while (at) {
-        const int e = __ffs(at) - 1;
-        at &= at - 1;
-        const uint32_t key = beam_key(pc.value_at(y, e));
-        if (key >= bound) beam_push(sh, key, i + e);
-      }
-    };
-    while (hits) {
-      const int v = __ffs(hits) - 1;
-      hits &= hits - 1;
-      gather(pc.load(v), pc.index(v));
-    }
-    if (edge_at >= 0 && key_top) gather(edge, edge_at * kPer - pc.mis);
     float s = (sum[0] + sum[1]) + (sum[2] + sum[3]);
 #pragma unroll
     for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
     if (lane == 0) sh.part[warp] = s;
     __syncthreads();
-    if (sh.count > kBeamCap) beam_bisect(&sh, row_x, p.n, piece, p.pieces, p.k);
+    if (key_top && (!gathered || sh.hits > kBeamHits || sh.count > kBeamCap)) beam_bisect(&sh, row_x, p.n, piece, p.pieces, p.k);
     const int found = sh.count;
-    for (int i = tid; i < found; i += kBeamThreads) {
-      const uint64_t e = sh.gathered[i];
-      int above = 0;
-#pragma unroll 4
-      for (int j = 0; j < found; ++j) above += sh.gathered[j] > e;
-      if (above < p.k) list[above] = e;
-    }
+    beam_rank(
+        found, [&](int j, int i) { return sh.gathered[j] > sh.gathered[i]; },
+        [&](int i, int above) {
+          if (above < p.k) list[above] = sh.gathered[i];
+        });
     for (int i = found + tid; i < p.k; i += kBeamThreads) list[i] = 0;
     if (tid == 0) {
       double t = 0.0;
 #pragma unroll
       for (int w = 0; w < kBeamThreads / 32; ++w) t += sh.part[w];
-      *sum_out = BeamSum{t * exp2(fix), key_top};
+      *sum_out = BeamSum{t, key_top, r};
     }
   }
-  __syncthreads();
-  if (tid == 0) {
-    const uint32_t n = static_cast<uint32_t>(p.beams) * p.pieces - 1;
-    __threadfence();
-    sh.last = atomicAdd(p.tickets + local, 1u) == n;
-    if (sh.last) p.tickets[local] = 0;
-    __threadfence();
-  }
-  __syncthreads();
-  if (!sh.last) return;
-  beam_finish(p, sh, local);
 }
 
 // ---------------------------------------------------------------- reordering

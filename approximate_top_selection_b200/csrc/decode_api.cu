@@ -21,7 +21,7 @@ namespace {
 
 // The part of a workspace that is zero between calls, of every operator.
 constexpr size_t kTicketBytes = TOPK_DECODE_TICKET_BYTES;
-static_assert(kTicketBytes >= 12 * kAttendMaxCtas && kTicketBytes >= 4 * kBeamTickets, "tickets");
+static_assert(kTicketBytes >= 12 * kAttendMaxCtas, "tickets");
 
 constexpr int kMaxReorder = 256;
 constexpr int64_t kMaxGridX = 2147483647LL;
@@ -156,10 +156,11 @@ struct BeamPlan {
 BeamPlan plan_beam(int64_t batch, int beams, int64_t n, int k, int esz, const DeviceInfo& dev) {
   BeamPlan pl;
   pl.pieces = beam_pieces(batch * beams, n, esz, dev);
-  // as many sentences as have tickets and fit a grid and about 1 GB of lists
-  const int64_t row_bytes = static_cast<int64_t>(pl.pieces) * (sizeof(BeamSum) + 8 * k) * beams;
-  const int64_t fit = std::min<int64_t>((int64_t{1} << 30) / row_bytes, kMaxGridX / (static_cast<int64_t>(pl.pieces) * beams));
-  pl.sentences = std::min(std::min(batch, static_cast<int64_t>(kBeamTickets)), std::max<int64_t>(fit, 1));
+  // as many sentences as fit a grid and about 1 GB of lists
+  const int64_t sentence_bytes = static_cast<int64_t>(pl.pieces) * (sizeof(BeamSum) + 8 * k) * beams;
+  const int64_t fit = std::min<int64_t>((int64_t{1} << 30) / sentence_bytes,
+                                        kMaxGridX / (static_cast<int64_t>(pl.pieces) * beams));
+  pl.sentences = std::min(batch, std::max<int64_t>(fit, 1));
   pl.sums = static_cast<size_t>(pl.sentences) * beams * pl.pieces * sizeof(BeamSum);
   pl.lists = static_cast<size_t>(pl.sentences) * beams * pl.pieces * k * 8;
   return pl;
@@ -179,15 +180,17 @@ int run_beam(const T* logits, const float* scores, int64_t batch, int beams, int
   const BeamPlan pl = plan_beam(batch, beams, n, k, sizeof(T), dev);
   if (!ws || ws_bytes < pl.total()) return TOPK_EWORKSPACE;
   if (!aligned16(ws)) return TOPK_EINVAL;
-  BeamArgs a{logits, scores, n, beams, k, pl.pieces, 0, out_scores, out_parent, out_token, nullptr, nullptr, nullptr};
+  BeamArgs a{logits, scores, n, beams, k, pl.pieces, 0, out_scores, out_parent, out_token, nullptr, nullptr};
   unsigned char* base = static_cast<unsigned char*>(ws);
-  a.tickets = reinterpret_cast<uint32_t*>(base);
   a.sums = reinterpret_cast<BeamSum*>(base + kTicketBytes);
   a.lists = reinterpret_cast<uint64_t*>(base + kTicketBytes + pl.sums);
   for (; a.first < batch; a.first += pl.sentences) {
-    const int64_t rows = std::min(pl.sentences, batch - a.first) * beams;
-    rc = launch_pdl(topk_beam_kernel<T>, dim3(static_cast<unsigned>(rows * pl.pieces)), dim3(kBeamThreads), 0,
-                    static_cast<cudaStream_t>(stream), a);
+    const int64_t sentences = std::min(pl.sentences, batch - a.first);
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if ((rc = launch_pdl(topk_beam_kernel<T>, dim3(static_cast<unsigned>(sentences * beams * pl.pieces)),
+                         dim3(kBeamThreads), 0, st, a)))
+      return rc;
+    rc = launch_pdl(beam_finish_kernel, dim3(static_cast<unsigned>(sentences)), dim3(kBeamThreads), 0, st, a);
     if (rc) return rc;
   }
   return TOPK_OK;
