@@ -113,9 +113,11 @@ Table table_of(PyObject* table_obj, PyObject* lens_obj, int64_t batch, int dev) 
   return Table{data<int32_t>(t), data<int32_t>(l), t.stride(0), static_cast<int>(t.size(1))};
 }
 
-// One workspace per (device, stream), as _decode.py keeps for its own calls.
-// Under stream capture a call gets one from the graph's memory: not usual.
-const at::Tensor& workspace(size_t bytes, int dev, cudaStream_t stream, const at::Tensor& like) {
+// One workspace per (device, stream), as _decode.py keeps for its own calls; the
+// caller holds it until its launch, while another thread may put a larger one
+// in its place.  Under stream capture a call gets one from the graph's memory:
+// not usual.
+at::Tensor workspace(size_t bytes, int dev, cudaStream_t stream, const at::Tensor& like) {
   cudaStreamCaptureStatus capture = cudaStreamCaptureStatusNone;
   usual(cudaStreamIsCapturing(stream, &capture) == cudaSuccess && capture == cudaStreamCaptureStatusNone);
   static auto* kept = new std::map<std::pair<int, cudaStream_t>, at::Tensor>();  // outlives the CUDA context
@@ -181,7 +183,7 @@ PyObject* call_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
     }
     const bool with_lse = a[9] == Py_True;
     const cudaStream_t stream = c10::cuda::getCurrentCUDAStream(dev).stream();
-    const at::Tensor& ws = workspace(g_lib.attend_bytes(1, 1, 0, static_cast<int>(d)), dev, stream, q);
+    const at::Tensor ws = workspace(g_lib.attend_bytes(1, 1, 0, static_cast<int>(d)), dev, stream, q);
     at::Tensor out = at::empty({batch, heads, d}, q.options());
     at::Tensor lse;
     if (with_lse) lse = at::empty({batch, heads}, q.options().dtype(at::kFloat));
@@ -251,7 +253,7 @@ PyObject* call_beam(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const cudaStream_t stream = c10::cuda::getCurrentCUDAStream(dev).stream();
     const size_t bytes = g_lib.beam_bytes(batch, static_cast<int>(beams), len, static_cast<int>(k));
     usual(bytes > 0);
-    const at::Tensor& ws = workspace(bytes, dev, stream, x);
+    const at::Tensor ws = workspace(bytes, dev, stream, x);
     at::Tensor score = at::empty({batch, k}, s.options());
     at::Tensor parent = at::empty({batch, k}, s.options().dtype(at::kInt));
     at::Tensor token = at::empty({batch, k}, s.options().dtype(at::kInt));

@@ -709,17 +709,6 @@ __global__ void __launch_bounds__(kAttendThreads, (AttendShape<D, kE4m3, NT>::kC
 
   const int units = p.lists * p.row_tiles;
   const int group = p.heads / p.lists;
-  // Sequences without a token have no granule: their rows are written here.
-  if (!p.positions) {
-    for (int b = blockIdx.x; b < p.tab.batch; b += gridDim.x) {
-      if (seq_length(p.tab, b) != 0) continue;
-      uint32_t* dst = reinterpret_cast<uint32_t*>(p.out + static_cast<int64_t>(b) * p.heads * D);
-      for (int i = tid; i < p.heads * D / 2; i += kAttendThreads) dst[i] = 0;
-      if (p.lse)
-        for (int i = tid; i < p.heads; i += kAttendThreads)
-          p.lse[static_cast<int64_t>(b) * p.heads + i] = __int_as_float(0xff800000);
-    }
-  }
   // This CTA's share [g0, g1) of the line, and where it begins.
   // No share is empty: shares are given to as many CTAs as there are granules.
   int64_t total, g0, g1;
@@ -745,7 +734,12 @@ __global__ void __launch_bounds__(kAttendThreads, (AttendShape<D, kE4m3, NT>::kC
     const int per = (p.tab.batch + kAttendThreads - 1) / kAttendThreads;
     const int b0 = min(tid * per, p.tab.batch), b1 = min(b0 + per, p.tab.batch);
     int64_t mine = 0;
-    for (int b = b0; b < b1; ++b) mine += granules_of<S::kGranule>(seq_length(p.tab, b));
+    bool empty = false;
+    for (int b = b0; b < b1; ++b) {
+      const int n = granules_of<S::kGranule>(seq_length(p.tab, b));
+      mine += n;
+      empty |= n == 0;
+    }
     int64_t upto = mine;
 #pragma unroll
     for (int x = 1; x < 32; x <<= 1) {
@@ -753,7 +747,17 @@ __global__ void __launch_bounds__(kAttendThreads, (AttendShape<D, kE4m3, NT>::kC
       if (lane >= x) upto += y;
     }
     if (lane == 31) plan[warp] = upto;
-    __syncthreads();
+    if (__syncthreads_or(empty)) {
+      // Sequences without a token have no granule: their rows are written here.
+      for (int b = blockIdx.x; b < p.tab.batch; b += gridDim.x) {
+        if (seq_length(p.tab, b) != 0) continue;
+        uint32_t* dst = reinterpret_cast<uint32_t*>(p.out + static_cast<int64_t>(b) * p.heads * D);
+        for (int i = tid; i < p.heads * (D / 2); i += kAttendThreads) dst[i] = 0;
+        if (p.lse)
+          for (int i = tid; i < p.heads; i += kAttendThreads)
+            p.lse[static_cast<int64_t>(b) * p.heads + i] = __int_as_float(0xff800000);
+      }
+    }
     total = 0;
     for (int w = 0; w < kAttendWarps; ++w) {
       if (w < warp) upto += plan[w];

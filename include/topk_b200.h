@@ -308,7 +308,9 @@ int cache_read(const topk_cache *cache, const int32_t *block_table_dev, int64_t 
  * p = softmax over j of scale * q[b][h] . K_j, and lse[b][h] = log sum_j
  * exp(scale * q[b][h] . K_j), over the tokens j < seq_lens[b], or over the
  * listed positions.  Query head h reads key-value head h / (heads / kv_heads).
- * Products, sums and softmax are float32; out is rounded once to bf16.
+ * Products, sums and softmax are float32 (a weight enters its product with V
+ * with 16 significant bits beside BF16 values, 11 beside E4M3 ones); out is
+ * rounded once to bf16.  Equal calls give equal bits.
  *   q_dev         bf16, sequence b at b * q_stride elements, [heads x d]
  *                 contiguous there; 16-byte aligned, q_stride a multiple of 8.
  *   heads         a multiple of kv_heads.
@@ -328,8 +330,9 @@ int cache_read(const topk_cache *cache, const int32_t *block_table_dev, int64_t 
  * A head with no token to attend to, or whose scores are all -inf, gives
  * zeros and an lse of -inf.
  * The workspace holds paged_attention_workspace_bytes(...) bytes, 16-byte
- * aligned.  Its first TOPK_DECODE_TICKET_BYTES must be zero before its first
- * use and are zero again after every call; the rest is scratch.  It serves any
+ * aligned, on the device of the call.  Its first TOPK_DECODE_TICKET_BYTES must
+ * be zero before its first use and are zero again after every call; the rest is
+ * scratch.  It serves any
  * later call of this operator or of topk_beam (not of the selections above),
  * and calls that overlap on the GPU must not share one. */
 #define TOPK_DECODE_TICKET_BYTES 16384

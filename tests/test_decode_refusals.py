@@ -203,3 +203,20 @@ def test_binding_refuses_wrong_tensors():
     bad(ValueError, atk.beam_reorder, x, par, out=torch.zeros(2, 3, 11, device=dev))
     bad(atk.TopkError, atk.beam_reorder, x, par, out=x)
     bad(ValueError, atk.beam_reorder, x[:, :, :0], par)
+
+
+def test_the_extension_module_leaves_unusual_calls_alone(lib):
+    from approximate_top_selection_b200 import _decode
+
+    calls = _decode._usual()
+    c = torch.zeros(2, 1, 4, 64, dtype=torch.bfloat16)
+    i = torch.zeros(1, 2, dtype=torch.int32)
+    assert calls.paged_attention(c[0], c, c, i, i[0], None, None, None, None, False) is None
+    assert calls.cache_write(c[0], c[0], c, c, i[0], None, None) is None
+    assert calls.cache_read(c, i, i[0], 4, None) is None
+    assert calls.topk_beam(torch.zeros(1, 2, 8), torch.zeros(1, 2), 2) is None
+    assert calls.beam_reorder([torch.zeros(1, 2, 8)], i) is None
+    assert calls.cache_read("no", "tensor", 3, -1, None) is None
+    assert calls.beam_reorder(None, None) is None
+    with pytest.raises(TypeError):
+        calls.topk_beam(c)
