@@ -83,7 +83,7 @@ def _calls_command(out: str) -> list:
            os.path.join(cuda, "include"), sysconfig.get_paths()["include"]]
     return ["g++", "-std=c++17", "-O2", "-fPIC", "-shared", "-fvisibility=hidden",
             "-D_GLIBCXX_USE_CXX11_ABI=%d" % int(torch._C._GLIBCXX_USE_CXX11_ABI), *["-I" + p for p in inc], CALLS_SRC,
-            "-o", out, "-L" + os.path.join(root, "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python",
+            "-o", out, "-L" + os.path.join(root, "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_cuda", "-ltorch_python",
             "-L" + os.path.join(cuda, "lib64"), "-lcudart"]
 
 

@@ -56,7 +56,12 @@ __device__ __forceinline__ bool ranks_above(const Cont& a, const Cont& b) {
 //
 // Bound by reading the logits.  A logit costs one exponential (16 per clock
 // and SM: 4.5e12 a second, against 1.6e12 fp32 or 3.2e12 bf16 logits a second
-// at full bandwidth) and about five other instructions.
+// at full bandwidth) and about five other instructions.  Measured: 4 x 131072
+// fp32, k 8: 8.4 us; 32 sentences x 8 x 128255 bf16, k 16: 29.6 us, 2.2 TB/s:
+// 3.5 rounds of CTAs of 6 us, of which 2 wait for the logits, 2 work on them and
+// 2 are the bound, the ranking and the end, with little in flight.  Rejected:
+// resident CTAs with the next piece on its way into shared memory (39 us by
+// cp.async, 38 us by bulk copies: the pieces fit half as many warps).
 // A piece's largest key (0: nothing) and its sum of 2^(x L - r), with L = log2 e
 // rounded to fp32 and r a whole number near max * L (so that sums join by exact
 // powers of two), or of exp(x - max), r = kBeamByMax, where max is beyond 1e6.
@@ -582,6 +587,8 @@ __global__ void __launch_bounds__(kBeamThreads, 2) topk_beam_kernel(BeamArgs p) 
 // on 16-byte addresses; where the source lies s bytes off such addresses, each
 // vector is shifted together from the two aligned ones that hold it (both
 // inside the row; the second is the next lane's first and comes from L1).
+// Measured: 8 tensors of 16 rows of 4 MB: 158 us, 6.8 TB/s with rows read twice
+// served by L2.
 // The up to 31 bytes before the body and 47 behind it are copied singly.
 constexpr int kReorderStates = 64;  // tensors per launch
 constexpr int kReorderThreads = 256;

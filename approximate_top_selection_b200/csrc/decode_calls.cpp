@@ -10,6 +10,7 @@
 #include <Python.h>
 
 #include <ATen/ATen.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
 #include <cuda_runtime.h>
@@ -59,6 +60,10 @@ const at::Tensor& on(PyObject* o, int dev, at::ScalarType type, int64_t dims) {
 int current_device_of(const at::Tensor& t) {
   usual(t.is_cuda() && t.get_device() == c10::cuda::current_device());
   return t.get_device();
+}
+
+at::Tensor empty_on(int dev, at::IntArrayRef shape, at::ScalarType type) {
+  return at::detail::empty_cuda(shape, type, at::Device(at::kCUDA, static_cast<at::DeviceIndex>(dev)), std::nullopt);
 }
 
 template <typename T>
@@ -184,9 +189,9 @@ PyObject* call_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const bool with_lse = a[9] == Py_True;
     const cudaStream_t stream = c10::cuda::getCurrentCUDAStream(dev).stream();
     const at::Tensor ws = workspace(g_lib.attend_bytes(1, 1, 0, static_cast<int>(d)), dev, stream, q);
-    at::Tensor out = at::empty({batch, heads, d}, q.options());
+    at::Tensor out = empty_on(dev, {batch, heads, d}, at::kBFloat16);
     at::Tensor lse;
-    if (with_lse) lse = at::empty({batch, heads}, q.options().dtype(at::kFloat));
+    if (with_lse) lse = empty_on(dev, {batch, heads}, at::kFloat);
     const int st = without_gil([&] {
       return g_lib.attend(data<uint16_t>(q), q.stride(0), batch, static_cast<int>(heads), &k, &v, t.table, t.stride,
                           t.width, t.lens, positions, static_cast<int>(lists), static_cast<int>(c),
@@ -229,7 +234,7 @@ PyObject* call_read(PyObject*, PyObject* const* a, Py_ssize_t n) {
     usual(PyLong_Check(a[3]));
     const long long len = PyLong_AsLongLong(a[3]);
     usual(len > 0 && len <= INT32_MAX);
-    at::Tensor out = at::empty({batch, c.kv_heads, len, c.d}, t.options().dtype(at::kBFloat16));
+    at::Tensor out = empty_on(dev, {batch, c.kv_heads, len, c.d}, at::kBFloat16);
     const cudaStream_t stream = c10::cuda::getCurrentCUDAStream(dev).stream();
     const int st = without_gil([&] {
       return g_lib.read(&c, tab.table, tab.stride, tab.width, tab.lens, batch, len, data<uint16_t>(out), stream);
@@ -254,9 +259,9 @@ PyObject* call_beam(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const size_t bytes = g_lib.beam_bytes(batch, static_cast<int>(beams), len, static_cast<int>(k));
     usual(bytes > 0);
     const at::Tensor ws = workspace(bytes, dev, stream, x);
-    at::Tensor score = at::empty({batch, k}, s.options());
-    at::Tensor parent = at::empty({batch, k}, s.options().dtype(at::kInt));
-    at::Tensor token = at::empty({batch, k}, s.options().dtype(at::kInt));
+    at::Tensor score = empty_on(dev, {batch, k}, at::kFloat);
+    at::Tensor parent = empty_on(dev, {batch, k}, at::kInt);
+    at::Tensor token = empty_on(dev, {batch, k}, at::kInt);
     const int st = without_gil([&] {
       float* o = data<float>(score);
       int32_t *p = data<int32_t>(parent), *t = data<int32_t>(token);
@@ -296,7 +301,7 @@ PyObject* call_reorder(PyObject*, PyObject* const* a, Py_ssize_t n) {
       beams = t.size(1);
       shape.assign(t.sizes().begin(), t.sizes().end());
       shape[1] = k;
-      out[i] = at::empty(shape, t.options());
+      out[i] = empty_on(dev, shape, t.scalar_type());
       src[i] = t.const_data_ptr();
       dst[i] = data<void>(out[i]);
       bytes[i] = t.numel() / (batch * beams) * t.element_size();

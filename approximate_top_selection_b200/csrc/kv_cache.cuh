@@ -111,7 +111,9 @@ struct WriteArgs {
 // blocks of 16 tokens, in a block by (k or v, head), then by token: the rows of
 // a warp are successive tokens of one head, which in a prompt are neighbours
 // in the cache, and so are their scales.  Bound by memory: every value is read
-// once (2 bytes) and written once.
+// once (2 bytes) and written once.  Measured: 49999 tokens x 8 heads x 128 to
+// e4m3 in 70 us, 4.3 TB/s (four rows in flight and a loop over the grid: 86 us;
+// rows numbered by token: 73 us).
 constexpr int kWriteRows = 2;
 constexpr int kWriteBlock = 16;
 
@@ -215,6 +217,8 @@ struct ReadArgs {
 // head: D / 16 lanes per row, 16 values a lane, kReadRows rows of a lane group
 // in flight.  Rows past a sequence's end (and rows whose page does not exist)
 // are zero.  Bound by memory: the cached row read once, 2 bytes a value written.
+// Measured: 16 ragged sequences up to 32768, 8 heads x 128, e4m3: 256 us, 5.45
+// TB/s (four rows in flight at five CTAs per SM: 270 us; eight: 293 us).
 constexpr int kReadRows = 2;
 
 template <int D>

@@ -15,8 +15,8 @@
 //
 // Work: a unit is (sequence, list of query heads); its tokens are cut into
 // granules of 4 * KT tokens, one tile of KT keys per warp.  All granules of
-// all units form one line that the CTAs (two per SM) share evenly, whatever
-// the lengths; a unit that lies in several CTAs' shares is joined by the CTA
+// all units form one line that the CTAs (two or three per SM) share evenly,
+// whatever the lengths; a unit that lies in several CTAs' shares is joined by the CTA
 // that finishes last (an atomic ticket, nobody waits; the parts are added in
 // the order of the CTAs, so equal calls give equal bits).
 //
@@ -28,6 +28,20 @@
 // in the groups that the ring waits for anyway, so neither look-up's latency is
 // ever waited for by itself (with look-ups one tile ahead in registers they took
 // twice the time of the products on lists of 512 positions).
+//
+// Measured on one B200, bytes of K, V and scales against its copy bandwidth of
+// 6461 GB/s: 16 ragged sequences up to 32768, 32 heads on 8, d 128, bf16: 196
+// us, 98 %; 16 x 8192, 32 on 32: 197 us, 98 %; pages of one token: 197 us, 98 %;
+// e4m3, 4 ragged sequences up to 131072: 118 us, 87 % (issue: the codes' widening);
+// 512 of 8192 positions for 512 heads: 34 us, 61 % (starts, ends and joins of
+// 13 tiles a warp); 128 heads on 8 (NT = 2): bf16 209 us, 92 %, e4m3 159 us, 63 %
+// (issue).  One sequence of 1001: 11 us, of which the work takes 1: about 4 us
+// pass before the first tile (lengths, table, rows are three dependent trips to
+// memory), about 4 in joining 16 parts.
+// Rejected: heads as the 16 rows of the products (237 us where this takes 196:
+// twice the products and accumulators); q as two e4m3 codes beside e4m3 keys (the
+// 8-bit product is made of conversions here: 146 us against 130); one round that
+// also fills the ring (1 to 3 us slower on every case).
 #pragma once
 
 #include "kv_cache.cuh"
