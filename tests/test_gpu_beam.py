@@ -267,3 +267,16 @@ def test_reorder_beyond_32_bits():
     o = atk.beam_reorder(x, p)
     for j, r in enumerate(p[0].tolist()):
         assert torch.equal(o[0, j], x[0, r])
+
+
+def test_rows_beyond_32_bits():
+    n = 1_200_000_001  # 2.4 GB of bf16; the row of the second beam starts off any boundary
+    x = torch.zeros(1, 2, n, dtype=torch.bfloat16, device=DEV)
+    x[0, 0, n - 1], x[0, 0, 5], x[0, 1, n - 2], x[0, 1, 1_073_741_824] = 30.0, 29.0, 31.0, 28.0
+    s = torch.tensor([[0.0, -1.5]], device=DEV)
+    val, parent, token = atk.topk_beam(x, s, 5)
+    off = [math.log(math.exp(30.0) + math.exp(29.0) + n - 2), math.log(math.exp(31.0) + math.exp(28.0) + n - 2)]
+    want = sorted([(30 - off[0], 0, n - 1), (29 - off[0], 0, 5), (29.5 - off[1], 1, n - 2), (26.5 - off[1], 1, 1_073_741_824)],
+                  reverse=True) + [(-off[0], 0, 0)]
+    assert list(zip(parent[0].tolist(), token[0].tolist())) == [w[1:] for w in want]
+    assert all(abs(float(a) - w[0]) <= 2.0 ** -14 for a, w in zip(val[0], want))

@@ -113,3 +113,80 @@ def test_beam_search_over_a_paged_cache_equals_recomputing():
         table, history = atk.beam_reorder([table, history], parent)
         scores, token = new, token.long()
     assert atk.topk_device_status() == 0
+
+
+def _attention_case(seed, lens):
+    g = torch.Generator(device=DEV).manual_seed(seed)
+    batch, page = len(lens), 16
+    width = -(-max(lens) // page)
+    q = torch.randn(batch, 8, 128, generator=g, device=DEV).bfloat16()
+    k, v = (torch.randn(batch * width, 2, page, 128, generator=g, device=DEV).bfloat16() for _ in range(2))
+    table = torch.randperm(batch * width, generator=g, device=DEV).view(batch, width).to(torch.int32)
+    return q, k, v, table, torch.tensor(lens, dtype=torch.int32, device=DEV)
+
+
+def test_eager_calls_side_by_side_on_two_streams():
+    """Both split work over the GPU and use their stream's workspace at the same time."""
+    cases = [_attention_case(i, [5000, 3000]) for i in range(2)]
+    beams = [(torch.randn(2, 4, 50000, device=DEV), torch.zeros(2, 4, device=DEV)) for _ in range(2)]
+    want = [(atk.paged_attention(*c), atk.topk_beam(*b, 8)) for c, b in zip(cases, beams)]
+    streams = [torch.cuda.Stream() for _ in cases]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(25):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got[i].append((atk.paged_attention(*cases[i]), atk.topk_beam(*beams[i], 8)))
+    torch.cuda.synchronize()
+    for i in range(2):
+        for o, b in got[i]:
+            assert torch.equal(o, want[i][0])
+            assert all(torch.equal(x, y) for x, y in zip(b, want[i][1]))
+
+
+def test_one_workspace_for_attention_and_beam_search_in_turn():
+    c = _attention_case(3, [4000, 17, 900])
+    x, s = torch.randn(3, 4, 70000, device=DEV), torch.zeros(3, 4, device=DEV)
+    need = max(atk.paged_attention_workspace_bytes(3, 8, 0, 128), atk.topk_beam_workspace_bytes(3, 4, 70000, 8))
+    ws = torch.zeros(need, dtype=torch.uint8, device=DEV)
+    ws[16384:] = 0xFF  # only the first bytes have to be zero
+    o, b = atk.paged_attention(*c), atk.topk_beam(x, s, 8)
+    for _ in range(3):
+        assert torch.equal(atk.paged_attention(*c, workspace=ws), o)
+        assert all(torch.equal(p, w) for p, w in zip(atk.topk_beam(x, s, 8, workspace=ws), b))
+        assert bool((ws[:16384] == 0).all())
+
+
+def test_one_query_for_all_sequences_and_one_table():
+    """Tensors broadcast over the batch: strides of zero."""
+    q, k, v, table, lens = _attention_case(4, [700, 700, 700])
+    lens.copy_(torch.tensor([700, 33, 0]))
+    one, row = q[:1].expand(3, 8, 128), table[:1].expand(3, -1)
+    got = atk.paged_attention(one, k, v, row, lens)
+    want = atk.paged_attention(one.contiguous(), k, v, row.contiguous(), lens)
+    assert torch.equal(got, want) and bool((got[2] == 0).all())
+
+
+def test_calls_with_everything_given_equal_the_usual_ones():
+    """The extension module's calls and the ones made step by step (a stream or an output given)."""
+    c = _attention_case(5, [2000, 100])
+    x, s = torch.randn(2, 4, 30001, device=DEV).bfloat16(), torch.zeros(2, 4, device=DEV)
+    here = torch.cuda.current_stream()
+    pos = torch.randint(-1, 2000, (2, 8, 77), device=DEV, dtype=torch.int32)
+    a, b = (atk.paged_attention(*c, positions=pos, return_lse=True, **kw) for kw in ({}, {"stream": here}))
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+    a, b = (atk.paged_attention(*c, scale=kw.pop("scale"), **kw) for kw in ({"scale": 0.5}, {"scale": 0.5, "stream": here}))
+    assert torch.equal(a, b) and torch.equal(a, atk.paged_attention(*c, scale=torch.tensor(0.5).item()))
+    a, b = (atk.cache_read(c[1], c[3], c[4], 50, **kw) for kw in ({}, {"stream": here}))
+    assert torch.equal(a, b)
+    a, b = (atk.topk_beam(x, s, 8, **kw) for kw in ({}, {"stream": here}))
+    assert all(torch.equal(p, q) for p, q in zip(a, b))
+    par = a[1][:, :4].contiguous()
+    a, b = (atk.beam_reorder([x, s], par, **kw) for kw in ({}, {"stream": here}))
+    assert all(torch.equal(p, q) for p, q in zip(a, b))
+    new = torch.randn(9, 2, 128, device=DEV).bfloat16()
+    slots = torch.randperm(c[1].shape[0] * 16, device=DEV)[:9]
+    k1, v1, k2, v2 = (t.clone() for t in (c[1], c[2], c[1], c[2]))
+    atk.cache_write(new, new, k1, v1, slots)
+    atk.cache_write(new, new, k2, v2, slots, stream=here)
+    assert torch.equal(k1, k2) and torch.equal(v1, v2) and not torch.equal(k1, c[1])
