@@ -35,6 +35,7 @@ int cache_view(const topk_cache* c, CacheView* v) {
   if (c->type != TOPK_CACHE_BF16 && c->type != TOPK_CACHE_E4M3) return TOPK_EINVAL;
   if (!cache_head_dim(c->d)) return TOPK_EUNSUPPORTED;
   if (c->pages > kMaxN) return TOPK_EUNSUPPORTED;  // page numbers are int32
+  if (c->kv_heads > (1 << 20)) return TOPK_EUNSUPPORTED;
   const int64_t esz = c->type == TOPK_CACHE_BF16 ? 2 : 1;
   if (!aligned16(c->data)) return TOPK_EINVAL;
   const int64_t strides[3] = {c->page_stride, c->head_stride, c->token_stride};
@@ -57,6 +58,11 @@ int cache_view(const topk_cache* c, CacheView* v) {
   v->pages = c->pages;
   v->kv_heads = c->kv_heads;
   v->page_size = c->page_size;
+  // t / page_size for t < 2^31 by a multiplication: 2^shift / page_size rounded up, shift = 31 + ceil(log2 page_size)
+  v->page_shift = 31;
+  while ((int64_t{1} << (v->page_shift - 31)) < c->page_size) ++v->page_shift;
+  v->page_magic = static_cast<uint32_t>(((static_cast<unsigned __int128>(1) << v->page_shift) + c->page_size - 1) /
+                                        static_cast<unsigned>(c->page_size));
   return TOPK_OK;
 }
 
@@ -115,9 +121,11 @@ int launch_write(const WriteArgs& a, const DeviceInfo& dev, cudaStream_t st) {
   int rc = prepare_kernel(cache_write_kernel<D, kE4m3>);
   if (rc) return rc;
   (void)dev;
-  const int64_t rows = (a.tokens + kWriteBlock - 1) / kWriteBlock * kWriteBlock * 2 * a.cache[0].kv_heads;
-  const int64_t grid = std::min((rows + write_rows_per_cta<D>() - 1) / write_rows_per_cta<D>(), kMaxGridX);
-  return launch_pdl(cache_write_kernel<D, kE4m3>, dim3(static_cast<unsigned>(grid)), dim3(256), 0, st, a);
+  const int64_t blocks = (a.tokens + kWriteTokens - 1) / kWriteTokens;
+  if (blocks > kMaxGridX) return TOPK_EUNSUPPORTED;
+  const int lines = (2 * a.cache[0].kv_heads + write_lines<D>() - 1) / write_lines<D>();
+  return launch_pdl(cache_write_kernel<D, kE4m3>,
+                    dim3(static_cast<unsigned>(blocks), static_cast<unsigned>(std::min(lines, 65535))), dim3(256), 0, st, a);
 }
 
 template <int D, bool kE4m3>
@@ -125,9 +133,11 @@ int launch_read(const ReadArgs& a, const DeviceInfo& dev, cudaStream_t st) {
   int rc = prepare_kernel(cache_read_kernel<D, kE4m3>);
   if (rc) return rc;
   (void)dev;
-  const int64_t blocks = (a.n + read_rows_per_cta<D>() - 1) / read_rows_per_cta<D>();
-  const int64_t grid = std::min(blocks * a.tab.batch * a.cache.kv_heads, kMaxGridX);
-  return launch_pdl(cache_read_kernel<D, kE4m3>, dim3(static_cast<unsigned>(grid)), dim3(256), 0, st, a);
+  const int64_t blocks = (a.n + read_rows<D>() - 1) / read_rows<D>();
+  return launch_pdl(cache_read_kernel<D, kE4m3>,
+                    dim3(static_cast<unsigned>(blocks), static_cast<unsigned>(std::min(a.cache.kv_heads, 65535)),
+                         static_cast<unsigned>(std::min(a.tab.batch, 65535))),
+                    dim3(256), 0, st, a);
 }
 
 // Picks the instantiation for (d, cache type).
@@ -243,11 +253,6 @@ int paged_attention(const uint16_t* q, int64_t q_stride, int64_t batch, int head
                    a.k.token_stride == a.v.token_stride &&
                    (!a.k.scale || (a.k.s_page_stride == a.v.s_page_stride && a.k.s_head_stride == a.v.s_head_stride &&
                                    a.k.s_token_stride == a.v.s_token_stride));
-  // t / page_size for t < 2^31 by a multiplication: 2^shift / page_size rounded up, shift = 31 + ceil(log2 page_size)
-  a.page_shift = 31;
-  while ((1LL << (a.page_shift - 31)) < k_cache->page_size) ++a.page_shift;
-  a.page_magic = static_cast<uint32_t>(((static_cast<unsigned __int128>(1) << a.page_shift) + k_cache->page_size - 1) /
-                                       static_cast<unsigned>(k_cache->page_size));
   a.grouped = !positions && k_cache->page_size % 16 == 0 && a.same_strides;
   a.q = q;
   a.q_stride = q_stride;

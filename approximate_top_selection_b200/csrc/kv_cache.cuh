@@ -28,6 +28,11 @@ struct CacheView {
   int64_t s_page_stride, s_head_stride, s_token_stride;  // elements of scale
   int64_t pages;
   int kv_heads, page_size;
+  uint32_t page_magic, page_shift;  // t / page_size = (t * page_magic) >> page_shift for 0 <= t < 2^31
+
+  __device__ __forceinline__ int page_of(int t) const {
+    return static_cast<int>((static_cast<uint64_t>(t) * page_magic) >> page_shift);
+  }
 };
 
 struct TableView {
@@ -72,11 +77,15 @@ __device__ __forceinline__ float2 f16x2_to_float2(uint32_t h) {
   return f;
 }
 
-// Two floats as e4m3 codes, a in the low byte (round to nearest even; the
-// callers keep |a|, |b| <= 448, so saturation never acts; NaN gives code 0x7F).
-__device__ __forceinline__ uint32_t floats_to_e4m3x2(float a, float b) {
-  uint16_t r;
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(b), "f"(a));
+// Four floats as e4m3 codes, a in the low byte (round to nearest even; the
+// callers keep magnitudes within 448, so saturation never acts; NaN gives code
+// 0x7F).
+__device__ __forceinline__ uint32_t floats_to_e4m3x4(float a, float b, float c, float d) {
+  uint32_t r;
+  asm("{\n\t.reg .b16 lo, hi;\n\tcvt.rn.satfinite.e4m3x2.f32 lo, %2, %1;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f32 hi, %4, %3;\n\tmov.b32 %0, {lo, hi};\n\t}"
+      : "=r"(r)
+      : "f"(a), "f"(b), "f"(c), "f"(d));
   return r;
 }
 
@@ -106,70 +115,67 @@ struct WriteArgs {
   int64_t tokens;
 };
 
-// D / 16 lanes per row, 16 values a lane, kWriteRows rows of a lane group in
-// flight; a CTA takes 256 / (D / 16) * kWriteRows rows.  Rows are numbered by
-// blocks of 16 tokens, in a block by (k or v, head), then by token: the rows of
-// a warp are successive tokens of one head, which in a prompt are neighbours
-// in the cache, and so are their scales.  Bound by memory: every value is read
-// once (2 bytes) and written once.  Measured: 49999 tokens x 8 heads x 128 to
-// e4m3 in 68 us, 4.4 TB/s (four rows in flight and a loop over the grid: 86 us;
-// rows numbered by token: 73 us).
-constexpr int kWriteRows = 2;
-constexpr int kWriteBlock = 16;
+// D / 16 lanes per row, 16 values a lane, two rows of a lane group in flight.  A
+// CTA takes 16 tokens (blockIdx.x) by write_lines() of the tokens' lines (k or
+// v, head; blockIdx.y), rows numbered by line, then token: the rows of a warp
+// are successive tokens of one head, which in a prompt are neighbours in the
+// cache, and so are their scales.  Bound by memory as far as bytes go (every
+// value read once, 2 bytes, and written once), but near the issue limit too: 16
+// values of a lane are widened, scaled and rounded in about 70 instructions, and
+// finding the row must not take more.  Measured: 49999 tokens x 8 heads x 128 to
+// e4m3 in 62 us, 4.9 TB/s (with 64-bit divisions for the row and the
+// page: 68 us, issue slots 75 % busy; rows numbered by token: 73 us).
+constexpr int kWriteTokens = 16;
 
 template <int D>
-__host__ __device__ constexpr int write_rows_per_cta() {
-  return 256 / (D / 16) * kWriteRows;
+__host__ __device__ constexpr int write_lines() {
+  return 2 * 256 / (D / 16) / kWriteTokens;
+}
+
+__device__ __noinline__ int64_t divide_wide(int64_t a, int64_t b) { return a / b; }
+
+__device__ __forceinline__ uint32_t larger_bf16x2(uint32_t a, uint32_t b) {  // NaN is the largest
+  uint32_t d;
+  asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
 }
 
 template <int D, bool kE4m3>
-__global__ void __launch_bounds__(256, 4) cache_write_kernel(WriteArgs p) {
-  constexpr int L = D / 16, kGroups = 256 / L;
+__global__ void __launch_bounds__(256, 5) cache_write_kernel(WriteArgs p) {
+  constexpr int L = D / 16, kGroups = 256 / L, kRows = 2;
   pdl_wait_then_release();
   const int heads = p.cache[0].kv_heads;
-  const int64_t block_rows = 2 * static_cast<int64_t>(heads) * kWriteBlock;
-  const int64_t rows = (p.tokens + kWriteBlock - 1) / kWriteBlock * block_rows;
   const int gl = threadIdx.x % L;
   const unsigned mask = ((1u << L) - 1u) << (threadIdx.x % 32 / L * L);
-  for (int64_t r0 = static_cast<int64_t>(blockIdx.x) * write_rows_per_cta<D>(); r0 < rows;
-       r0 += static_cast<int64_t>(gridDim.x) * write_rows_per_cta<D>()) {
-    const int64_t block0 = r0 / block_rows, in_block = r0 - block0 * block_rows;
-    int64_t slot[kWriteRows];
-    int64_t tok[kWriteRows];
-    int ln[kWriteRows];
+  const int64_t t0 = static_cast<int64_t>(blockIdx.x) * kWriteTokens;
+  for (int line0 = blockIdx.y * write_lines<D>(); line0 < 2 * heads; line0 += gridDim.y * write_lines<D>()) {
+    int64_t slot[kRows];
+    uint4 x[kRows][2];
 #pragma unroll
-    for (int i = 0; i < kWriteRows; ++i) {
-      int64_t j = in_block + i * kGroups + threadIdx.x / L, block = block0;
-      while (j >= block_rows) {  // at most a few blocks on: a CTA has 128 rows, a block 32 or more
-        j -= block_rows;
-        ++block;
-      }
-      ln[i] = static_cast<int>(j / kWriteBlock);
-      tok[i] = block * kWriteBlock + j % kWriteBlock;
-      slot[i] = tok[i] < p.tokens ? __ldg(p.slots + tok[i]) : -1;
-    }
-    uint4 x[kWriteRows][2];
-#pragma unroll
-    for (int i = 0; i < kWriteRows; ++i) {
-      const int w = ln[i] >= heads ? 1 : 0, h = ln[i] - w * heads;
-      const uint4* src = reinterpret_cast<const uint4*>((w ? p.src[1] : p.src[0]) +
-                                                        tok[i] * (w ? p.token_stride[1] : p.token_stride[0]) +
-                                                        h * (w ? p.head_stride[1] : p.head_stride[0])) +
-                         gl * 2;
+    for (int i = 0; i < kRows; ++i) {
+      const int j = i * kGroups + static_cast<int>(threadIdx.x) / L;
+      const int64_t t = t0 + j % kWriteTokens;
+      const int line = line0 + j / kWriteTokens;
+      const bool live = t < p.tokens && line < 2 * heads;
+      const int w = line >= heads ? 1 : 0;
+      slot[i] = live ? __ldg(p.slots + t) : -1;
       x[i][0] = x[i][1] = make_uint4(0, 0, 0, 0);
-      if (tok[i] < p.tokens) {  // not waiting for the slot
+      if (live) {  // not waiting for the slot
+        const uint4* src = reinterpret_cast<const uint4*>((w ? p.src[1] : p.src[0]) +
+                                                          t * (w ? p.token_stride[1] : p.token_stride[0]) +
+                                                          (line - w * heads) * (w ? p.head_stride[1] : p.head_stride[0])) +
+                           gl * 2;
         x[i][0] = __ldcs(src);
         x[i][1] = __ldcs(src + 1);
       }
     }
 #pragma unroll
-    for (int i = 0; i < kWriteRows; ++i) {
+    for (int i = 0; i < kRows; ++i) {
       if (slot[i] < 0) continue;  // the same for a group's lanes
-      const int w = ln[i] >= heads ? 1 : 0, h = ln[i] - w * heads;
+      const int line = line0 + (i * kGroups + static_cast<int>(threadIdx.x) / L) / kWriteTokens;
+      const int w = line >= heads ? 1 : 0, h = line - w * heads;
       const CacheView& c = p.cache[w];
-      const int64_t page = (slot[i] >> 32) == 0
-                               ? static_cast<int64_t>(static_cast<uint32_t>(slot[i]) / static_cast<uint32_t>(c.page_size))
-                               : slot[i] / c.page_size;
+      const int64_t page = slot[i] <= 0x7fffffff ? c.page_of(static_cast<int>(slot[i])) : divide_wide(slot[i], c.page_size);
       if (page >= c.pages) {
         atomicOr(&g_device_status, kDevBadIndex);
         continue;
@@ -181,21 +187,21 @@ __global__ void __launch_bounds__(256, 4) cache_write_kernel(WriteArgs p) {
         reinterpret_cast<uint4*>(dst)[gl * 2 + 1] = x[i][1];
       } else {
         const uint32_t xs[8] = {x[i][0].x, x[i][0].y, x[i][0].z, x[i][0].w, x[i][1].x, x[i][1].y, x[i][1].z, x[i][1].w};
-        uint32_t top = 0;
+        uint32_t both = 0;  // the largest magnitudes of the even and the odd values
 #pragma unroll
-        for (int y = 0; y < 8; ++y) top = max(top, max((xs[y] << 16) & 0x7fff0000u, xs[y] & 0x7fff0000u));
+        for (int y = 0; y < 8; ++y) both = larger_bf16x2(both, xs[y] & 0x7fff7fffu);
 #pragma unroll
-        for (int o = L / 2; o >= 1; o >>= 1) top = max(top, __shfl_xor_sync(mask, top, o));
+        for (int o = L / 2; o >= 1; o >>= 1) both = larger_bf16x2(both, __shfl_xor_sync(mask, both, o));
+        const uint32_t top = max(both << 16, both & 0xffff0000u);
         const bool finite = top < 0x7f800000u;
         const int e = row_exponent(top);
         const float inv = finite ? power_of_two(-e) : __uint_as_float(0x7fffffffu);
         uint32_t out[4];
 #pragma unroll
         for (int y = 0; y < 4; ++y)
-          out[y] = floats_to_e4m3x2(__uint_as_float(xs[2 * y] << 16) * inv, __uint_as_float(xs[2 * y] & 0xffff0000u) * inv) |
-                   (floats_to_e4m3x2(__uint_as_float(xs[2 * y + 1] << 16) * inv,
-                                     __uint_as_float(xs[2 * y + 1] & 0xffff0000u) * inv)
-                    << 16);
+          out[y] = floats_to_e4m3x4(__uint_as_float(xs[2 * y] << 16) * inv, __uint_as_float(xs[2 * y] & 0xffff0000u) * inv,
+                                    __uint_as_float(xs[2 * y + 1] << 16) * inv,
+                                    __uint_as_float(xs[2 * y + 1] & 0xffff0000u) * inv);
         reinterpret_cast<uint4*>(dst)[gl] = make_uint4(out[0], out[1], out[2], out[3]);
         if (gl == 0)
           c.scale[page * c.s_page_stride + h * c.s_head_stride + off * c.s_token_stride] =
@@ -213,86 +219,85 @@ struct ReadArgs {
   uint16_t* out;  // [batch][kv_heads][n][d] bf16
 };
 
-// A CTA reads 256 / (D / 16) * kReadRows successive rows of one sequence and
-// head: D / 16 lanes per row, 16 values a lane, kReadRows rows of a lane group
-// in flight.  Rows past a sequence's end (and rows whose page does not exist)
-// are zero.  Bound by memory: the cached row read once, 2 bytes a value written.
-// Measured: 16 ragged sequences up to 32768, 8 heads x 128, e4m3: 256 us, 5.45
-// TB/s (four rows in flight at five CTAs per SM: 270 us; eight: 293 us).
-constexpr int kReadRows = 2;
-
+// A CTA reads read_rows() successive rows (blockIdx.x) of one head (blockIdx.y)
+// of one sequence (blockIdx.z): D / 16 lanes per row, 16 values a lane, two rows
+// of a lane group in flight.  Rows past a sequence's end (and rows whose page
+// does not exist) are zero.  Bound by memory: the cached row read once, 2 bytes
+// a value written.  Measured: 16 ragged sequences up to 32768, 8 heads x 128,
+// e4m3: 254 us, 5.5 TB/s (with 64-bit divisions for sequence and head: 256
+// us, issue slots 75 % busy).
 template <int D>
-__host__ __device__ constexpr int read_rows_per_cta() {
-  return 256 / (D / 16) * kReadRows;
+__host__ __device__ constexpr int read_rows() {
+  return 2 * 256 / (D / 16);
 }
 
 template <int D, bool kE4m3>
-__global__ void __launch_bounds__(256, 8) cache_read_kernel(ReadArgs p) {
-  constexpr int L = D / 16, kGroups = 256 / L;
+__global__ void __launch_bounds__(256, 6) cache_read_kernel(ReadArgs p) {
+  constexpr int L = D / 16, kGroups = 256 / L, kRows = 2;
   pdl_wait_then_release();
   const CacheView& c = p.cache;
-  const int64_t blocks = (p.n + read_rows_per_cta<D>() - 1) / read_rows_per_cta<D>();  // of a sequence and head
-  const int64_t items = blocks * p.tab.batch * c.kv_heads;
   const int gl = threadIdx.x % L, g = threadIdx.x / L;
-  for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
-    const int64_t bh = item / blocks;
-    const int b = static_cast<int>(bh / c.kv_heads), h = static_cast<int>(bh - static_cast<int64_t>(b) * c.kv_heads);
-    const int64_t t0 = (item - bh * blocks) * read_rows_per_cta<D>() + g;
+  const int64_t t0 = static_cast<int64_t>(blockIdx.x) * read_rows<D>() + g;
+  for (int b = blockIdx.z; b < p.tab.batch; b += gridDim.z) {
     const int len = seq_length(p.tab, b);
-    int32_t page[kReadRows];
-    int off[kReadRows];
+    for (int h = blockIdx.y; h < c.kv_heads; h += gridDim.y) {
+      int32_t page[kRows];
+      int off[kRows];
 #pragma unroll
-    for (int i = 0; i < kReadRows; ++i) {
-      const int64_t t = t0 + i * kGroups;
-      page[i] = -1;
-      off[i] = 0;
-      if (t < len && t < p.n) {
-        const int at = static_cast<int>(t) / c.page_size;
-        off[i] = static_cast<int>(t) - at * c.page_size;
-        page[i] = __ldg(p.tab.table + b * p.tab.stride + at);
-        if (page[i] < 0 || page[i] >= c.pages) {
-          atomicOr(&g_device_status, kDevBadIndex);
-          page[i] = -1;
+      for (int i = 0; i < kRows; ++i) {
+        const int64_t t = t0 + i * kGroups;
+        page[i] = -1;
+        off[i] = 0;
+        if (t < len && t < p.n) {
+          const int at = c.page_of(static_cast<int>(t));
+          off[i] = static_cast<int>(t) - at * c.page_size;
+          page[i] = __ldg(p.tab.table + b * p.tab.stride + at);
+          if (page[i] < 0 || page[i] >= c.pages) {
+            atomicOr(&g_device_status, kDevBadIndex);
+            page[i] = -1;
+          }
         }
       }
-    }
-    uint4 x[kReadRows][2];
-    float s[kReadRows];
+      uint4 x[kRows][2];
+      float s[kRows];
 #pragma unroll
-    for (int i = 0; i < kReadRows; ++i) {
-      x[i][0] = x[i][1] = make_uint4(0, 0, 0, 0);
-      s[i] = 0.0f;
-      if (page[i] >= 0) {
-        const uint4* src = reinterpret_cast<const uint4*>(c.data + page[i] * c.page_stride + h * c.head_stride +
-                                                          off[i] * c.token_stride);
+      for (int i = 0; i < kRows; ++i) {
+        x[i][0] = x[i][1] = make_uint4(0, 0, 0, 0);
+        s[i] = 0.0f;
+        if (page[i] >= 0) {
+          const uint4* src = reinterpret_cast<const uint4*>(c.data + page[i] * c.page_stride + h * c.head_stride +
+                                                            off[i] * c.token_stride);
+          if constexpr (kE4m3) {
+            x[i][0] = __ldg(src + gl);
+            s[i] = __ldg(c.scale + page[i] * c.s_page_stride + h * c.s_head_stride + off[i] * c.s_token_stride);
+          } else {
+            x[i][0] = __ldg(src + gl * 2);
+            x[i][1] = __ldg(src + gl * 2 + 1);
+          }
+        }
+      }
+      uint4* dst = reinterpret_cast<uint4*>(p.out + ((static_cast<int64_t>(b) * c.kv_heads + h) * p.n + t0) * D) + gl * 2;
+#pragma unroll
+      for (int i = 0; i < kRows; ++i) {
+        if (t0 + i * kGroups >= p.n) continue;
+        uint4 o0 = x[i][0], o1 = x[i][1];
         if constexpr (kE4m3) {
-          x[i][0] = __ldg(src + gl);
-          s[i] = __ldg(c.scale + page[i] * c.s_page_stride + h * c.s_head_stride + off[i] * c.s_token_stride);
-        } else {
-          x[i][0] = __ldg(src + gl * 2);
-          x[i][1] = __ldg(src + gl * 2 + 1);
-        }
-      }
-    }
+          const uint32_t w[4] = {x[i][0].x, x[i][0].y, x[i][0].z, x[i][0].w};
+          uint32_t o[8];
 #pragma unroll
-    for (int i = 0; i < kReadRows; ++i) {
-      const int64_t t = t0 + i * kGroups;
-      if (t >= p.n) continue;
-      uint4 o0 = x[i][0], o1 = x[i][1];
-      if constexpr (kE4m3) {
-        const uint32_t w[4] = {x[i][0].x, x[i][0].y, x[i][0].z, x[i][0].w};
-        uint32_t o[8];
-#pragma unroll
-        for (int y = 0; y < 8; ++y) {
-          const float2 f = f16x2_to_float2(e4m3x2_to_f16x2(y & 1 ? w[y / 2] >> 16 : w[y / 2] & 0xffffu));
-          o[y] = floats_to_bf16x2(f.x * s[i], f.y * s[i]);
+          for (int y = 0; y < 4; ++y) {
+            uint32_t low, high;
+            e4m3x4_to_f16x2(w[y], low, high);
+            const float2 a = f16x2_to_float2(low), z = f16x2_to_float2(high);
+            o[2 * y] = floats_to_bf16x2(a.x * s[i], a.y * s[i]);
+            o[2 * y + 1] = floats_to_bf16x2(z.x * s[i], z.y * s[i]);
+          }
+          o0 = make_uint4(o[0], o[1], o[2], o[3]);
+          o1 = make_uint4(o[4], o[5], o[6], o[7]);
         }
-        o0 = make_uint4(o[0], o[1], o[2], o[3]);
-        o1 = make_uint4(o[4], o[5], o[6], o[7]);
+        __stcs(dst + i * kGroups * (D / 8), o0);
+        __stcs(dst + i * kGroups * (D / 8) + 1, o1);
       }
-      uint4* dst = reinterpret_cast<uint4*>(p.out + (bh * p.n + t) * D) + gl * 2;
-      __stcs(dst, o0);
-      __stcs(dst + 1, o1);
     }
   }
 }

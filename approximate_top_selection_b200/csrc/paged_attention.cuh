@@ -56,7 +56,6 @@ struct AttendArgs {
   const int32_t* positions;  // null, or [batch][lists][c]
   int heads, lists, c;
   int row_tiles;      // groups of 16 query heads per list
-  uint32_t page_magic, page_shift;  // t / page_size = (t * page_magic) >> page_shift for 0 <= t < 2^31
   bool grouped;       // no positions, 16 | page_size (16 tokens from a multiple of 16 on share a page), same strides
   bool same_strides;  // k and v, and their scales, have equal strides
   float scale_log2;   // softmax scale * log2(e)
@@ -838,7 +837,7 @@ __global__ void __launch_bounds__(kAttendThreads, (AttendShape<D, kE4m3, NT>::kC
         tok = p.positions ? tokens[slot * S::kKeys + lane] : static_cast<int>(i);
       const bool on = tok >= 0 && tok < place.z;
       if (tok >= p.tab.capacity) atomicOr(&g_device_status, kDevBadIndex);
-      const int at = on ? static_cast<int>((static_cast<uint64_t>(tok) * p.page_magic) >> p.page_shift) : 0;
+      const int at = on ? p.k.page_of(tok) : 0;
       copy4(pages_addr + (slot * S::kKeys + lane) * 4, p.tab.table + place.x * p.tab.stride + at, on);
       tokens[slot * S::kKeys + lane] = on ? tok - at * p.k.page_size : -1;
     }
