@@ -62,6 +62,7 @@ __device__ __forceinline__ bool ranks_above(const Cont& a, const Cont& b) {
 // 2 are the bound, the ranking and the end, with little in flight.  Rejected:
 // resident CTAs with the next piece on its way into shared memory (39 us by
 // cp.async, 38 us by bulk copies: the pieces fit half as many warps).
+
 // A piece's largest key (0: nothing) and its sum of 2^(x L - r), with L = log2 e
 // rounded to fp32 and r a whole number near max * L (so that sums join by exact
 // powers of two), or of exp(x - max), r = kBeamByMax, where max is beyond 1e6.
@@ -90,7 +91,7 @@ struct BeamArgs {
 constexpr int kMaxBeams = 128;
 constexpr int kBeamCap = 512;       // gathered candidates; more than the largest k
 constexpr int kBeamHits = 384;      // vectors that hold them
-constexpr int kBeamVectors = 16;   // 16-byte vectors per thread
+constexpr int kBeamVectors = 16;    // 16-byte vectors per thread
 
 // Order key of a candidate logit; 0 for one that gives no continuation.
 __device__ __forceinline__ uint32_t beam_key(float x) {
@@ -587,9 +588,9 @@ __global__ void __launch_bounds__(kBeamThreads, 2) topk_beam_kernel(BeamArgs p) 
 // on 16-byte addresses; where the source lies s bytes off such addresses, each
 // vector is shifted together from the two aligned ones that hold it (both
 // inside the row; the second is the next lane's first and comes from L1).
-// Measured: 8 tensors of 16 rows of 4 MB: 158 us, 6.8 TB/s with rows read twice
-// served by L2.
 // The up to 31 bytes before the body and 47 behind it are copied singly.
+// Measured: 8 tensors of 16 rows of 4 MB: 158 us, 6.8 TB/s (rows read twice come
+// from L2 the second time).
 constexpr int kReorderStates = 64;  // tensors per launch
 constexpr int kReorderThreads = 256;
 constexpr int kReorderUnroll = 8;
