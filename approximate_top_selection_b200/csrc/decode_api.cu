@@ -93,19 +93,45 @@ size_t attend_workspace(int d, const DeviceInfo& dev) {
   return kTicketBytes + static_cast<size_t>(ctas) * 2 * attend_part_floats(d) * 4;
 }
 
+// Whether warps take whole units, each one by itself.  It saves the joins of
+// the warps and CTAs (2 us or more of a CTA's time per unit) and costs the
+// evenness of shares, and the time that a unit takes in one warp.  So: a unit
+// of one tile always; else as many units as keep the CTAs loading, two per CTA
+// where a unit has four granules (a warp's 16 tiles), one per warp at eight,
+// and lists, which are all of one length, only in nearly full rounds of the
+// warps.  Measured (one way, the other; us; d 128, 8 key heads unless said):
+// 85 sequences of up to 3 tokens 6.3, 14.5; 148 of up to 64: 9.3, 18.5; 74 of up to 256:
+// 21, 26; 37 of up to 256: 19.3, 18.7; 222 of up to 512: 61, 72; 74 of up to 512: 37, 38;
+// 222 of up to 1024: 114, 103; e4m3, 111 of up to 512: 27, 41; 128 heads on 8, 148 of up
+// to 512: 48, 98; d 256, 74 of up to 512: 46, 74; lists of 512 from 4096, 2560 of
+// them (72 % of three rounds): 129, 118, 3552 (all of three rounds): 142, 153.
+bool attend_solo(int64_t units, int64_t granules, bool one_tile, bool lists, int64_t ctas) {
+  if (one_tile) return true;
+  const int64_t warps = kAttendWarps * ctas;
+  if (lists && units > warps && granules > 2) return 7 * units >= 6 * ((units + warps - 1) / warps) * warps;
+  return granules <= 8 && 2 * units >= std::max<int64_t>(granules, 2) * ctas;
+}
+
 template <int D, bool kE4m3, int NT>
 int launch_attend_rows(AttendArgs& a, const DeviceInfo& dev, cudaStream_t st) {
   using S = AttendShape<D, kE4m3, NT>;
   if (S::kSmem > dev.max_smem_optin) return TOPK_EUNSUPPORTED;
-  int rc, per_sm = 0;
-  if ((rc = occupancy(paged_attention_kernel<D, kE4m3, NT>, kAttendThreads, S::kSmem, &per_sm))) return rc;
-  const int64_t most = a.positions ? a.c : a.tab.capacity;
+  const int64_t most = a.positions ? a.c : a.tab.capacity;  // tokens of a unit
   const int64_t granules = (most + S::kGranule - 1) / S::kGranule;
   const int64_t units = static_cast<int64_t>(a.lists) * a.row_tiles * a.tab.batch;
+  int rc, per_sm = 0;
+  if constexpr (!S::kQShared) {
+    if ((rc = occupancy(paged_attention_kernel<D, kE4m3, NT, true>, kAttendThreads, S::kSmem, &per_sm))) return rc;
+    const int64_t ctas = std::min(per_sm, kAttendCtasPerSm) * dev.sms;
+    if (attend_solo(units, granules, most <= S::kKeys, a.positions != nullptr, ctas))
+      return launch_pdl(paged_attention_kernel<D, kE4m3, NT, true>, dim3(static_cast<unsigned>(std::min(ctas, units))),
+                        dim3(kAttendThreads), S::kSmem, st, a);
+  }
+  if ((rc = occupancy(paged_attention_kernel<D, kE4m3, NT, false>, kAttendThreads, S::kSmem, &per_sm))) return rc;
   int64_t ctas = std::min(std::min(per_sm, kAttendCtasPerSm) * dev.sms, kAttendMaxCtas);
   if (granules <= ctas / units) ctas = std::max<int64_t>(1, granules * units);
-  return launch_pdl(paged_attention_kernel<D, kE4m3, NT>, dim3(static_cast<unsigned>(ctas)), dim3(kAttendThreads),
-                    S::kSmem, st, a);
+  return launch_pdl(paged_attention_kernel<D, kE4m3, NT, false>, dim3(static_cast<unsigned>(ctas)),
+                    dim3(kAttendThreads), S::kSmem, st, a);
 }
 
 template <int D, bool kE4m3>

@@ -132,6 +132,39 @@ def test_many_short_sequences():
 
 
 @pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+@pytest.mark.parametrize("batch,heads,kv_heads,d,page,longest", [
+    (50, 16, 16, 64, 16, 47),
+    (50, 16, 16, 128, 12, 47),
+    (35, 36, 18, 256, 5, 40),
+    (9, 40, 2, 128, 3, 11),      # three groups of a key head's 20 query heads
+    (3, 700, 350, 64, 7, 33),
+    (2, 512, 256, 256, 1, 30),
+])
+def test_many_short_units(kind, batch, heads, kv_heads, d, page, longest):
+    lens = [(i * 13) % (longest + 1) for i in range(batch - 1)] + [longest]
+    s = make(batch, heads, kv_heads, d, page, lens, kind, longest + d)
+    got = call(on_gpu(s))
+    check(s, got)
+    again = call(on_gpu(s))
+    assert all(torch.equal(x, y) for x, y in zip(got, again))
+    assert atk.topk_device_status() == 0
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+@pytest.mark.parametrize("heads,kv_heads,lists,d,c,batch", [(250, 5, 250, 128, 70, 30), (256, 2, 128, 64, 150, 60),
+                                                            (600, 3, 300, 256, 37, 17), (288, 2, 24, 128, 33, 200)])
+def test_many_lists(kind, heads, kv_heads, lists, d, c, batch):
+    g = torch.Generator().manual_seed(c)
+    lens = [(i * 37) % 101 for i in range(batch)]
+    s = make(batch, heads, kv_heads, d, 8, lens, kind, c + d)
+    s["positions"] = torch.randint(-1, 104, (batch, lists, c), generator=g, dtype=torch.int32)
+    check(s, call(on_gpu(s)))
+    # positions behind a sequence's end are left out; those behind its table's end are also reported
+    beyond = bool((s["positions"] >= s["table"].shape[1] * 8).any())
+    assert atk.topk_device_status() == (2 if beyond else 0)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
 @pytest.mark.parametrize("heads,kv_heads,lists,d,c", [(8, 2, 2, 128, 50), (8, 2, 8, 128, 33), (8, 2, 4, 64, 1),
                                                       (4, 4, 4, 256, 200), (32, 1, 1, 128, 700)])
 def test_listed_positions(kind, heads, kv_heads, lists, d, c):
