@@ -65,6 +65,13 @@ def _same_device(first: torch.Tensor, **others) -> None:
             raise ValueError("%s is on %s, not on %s" % (name, t.device, first.device))
 
 
+def _int32(**sizes) -> None:
+    """Sizes that the C interface takes as int: ctypes would cut off what does not fit."""
+    for name, n in sizes.items():
+        if not -2 ** 31 <= n < 2 ** 31:
+            raise ValueError("%s = %d does not fit 32 bits" % (name, n))
+
+
 def _check_cache(data: torch.Tensor, scale, name: str) -> None:
     if isinstance(data, torch.Tensor) and data.dtype == _E4M3:
         _cuda_strided(data, name, _E4M3, 4)
@@ -97,6 +104,7 @@ def _cache(data: torch.Tensor, scale, name: str, dev: int):
         _check_cache(data, scale, name)
         if data.get_device() != dev:
             raise ValueError("%s is on %s, not on cuda:%d" % (name, data.device, dev))
+    _int32(kv_heads=shape[1], page_size=shape[2], d=shape[3])
     if scale is None:
         return TopkCache(data.data_ptr(), None, *shape, TOPK_CACHE_BF16, *strides[:3], 0, 0, 0), shape
     return TopkCache(data.data_ptr(), scale.data_ptr(), *shape, TOPK_CACHE_E4M3, *strides[:3], *scale.stride()), shape
@@ -115,7 +123,7 @@ def _table(block_table, seq_lens, batch, dev):
         (rows, width), (stride, inner) = block_table.shape, block_table.stride()
         if (block_table.get_device() == dev and block_table.dtype is _I32 and inner == 1 and rows == batch and width > 0
                 and seq_lens.get_device() == dev and seq_lens.dtype is _I32 and seq_lens.shape == (batch,)
-                and (batch == 1 or seq_lens.stride() == (1,))):
+                and width < 2 ** 31 and (batch == 1 or seq_lens.stride() == (1,))):
             return stride, width
     except (AttributeError, TypeError, ValueError):
         pass
@@ -125,6 +133,7 @@ def _table(block_table, seq_lens, batch, dev):
         raise ValueError("block_table must be [batch, width] and seq_lens [batch]")
     if block_table.shape[1] < 1:
         raise ValueError("block_table needs a column at least")
+    _int32(width=block_table.shape[1])
     for name, t in (("block_table", block_table), ("seq_lens", seq_lens)):
         if t.get_device() != dev:
             raise ValueError("%s is on %s, not on cuda:%d" % (name, t.device, dev))
@@ -251,6 +260,7 @@ def paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
         lists, c = positions.shape[1:]
         if lists < 1 or c < 1 or lists % kv_heads or heads % lists:
             raise ValueError("positions needs c >= 1 and lists a multiple of kv_heads that divides heads")
+    _int32(heads=heads, lists=lists, c=c)
     if workspace is not None:
         _same_device(q, workspace=workspace)
 
@@ -379,6 +389,7 @@ def topk_beam(logits: torch.Tensor, beam_scores: torch.Tensor, k: int, *, out_sc
     if workspace is not None:
         _same_device(logits, workspace=workspace)
     batch, beams, n = logits.shape
+    _int32(beams=beams, k=k)
 
     def body(out_scores, out_parent, out_token, ws, sh):
         shape = (batch, max(k, 0))
@@ -431,6 +442,7 @@ def beam_reorder(states, parents: torch.Tensor, *, out=None, stream=None):
         if n == 0:
             raise ValueError("states must not be empty")
         sizes.append(n // (batch * beams) * t.element_size())
+    _int32(beams=beams, k=k)
     if out is not None:
         out = [out] if isinstance(out, torch.Tensor) else list(out)
         if len(out) != len(src):

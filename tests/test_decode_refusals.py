@@ -205,6 +205,36 @@ def test_binding_refuses_wrong_tensors():
     bad(ValueError, atk.beam_reorder, x[:, :, :0], par)
 
 
+def test_sizes_beyond_32_bits_are_refused():
+    from approximate_top_selection_b200 import _decode
+
+    big = 2 ** 32 + 2
+
+    def meta(*shape, dtype=torch.bfloat16):  # no memory; on device -1 as CPU tensors are
+        return torch.empty(*shape, dtype=dtype, device="meta")
+
+    for shape in ((1, big, 1, 64), (1, 1, big, 64), (1, 1, 1, big)):
+        with pytest.raises(ValueError, match="32 bits"):
+            _decode._cache(meta(*shape), None, "k_cache", -1)
+    assert _decode._cache(meta(big, 1, 1, 64), None, "k_cache", -1)[0].pages == big  # pages are 64-bit
+    with pytest.raises((TypeError, ValueError)):
+        _decode._table(meta(1, big, dtype=torch.int32), meta(1, dtype=torch.int32), 1, -1)
+    assert _decode._table(meta(1, 5, dtype=torch.int32), meta(1, dtype=torch.int32), 1, -1) == (5, 5)
+    for name in ("heads", "lists", "c", "beams", "k"):
+        _decode._int32(**{name: 2 ** 31 - 1})
+        with pytest.raises(ValueError, match="32 bits"):
+            _decode._int32(**{name: 2 ** 31})
+
+
+@pytest.mark.gpu
+def test_a_beam_of_more_than_32_bits_is_refused():
+    x, s = torch.zeros(1, 3, 10, device="cuda:0"), torch.zeros(1, 3, device="cuda:0")
+    with pytest.raises(ValueError):
+        atk.topk_beam(x, s, 2 ** 32 + 2)
+    with pytest.raises(ValueError):
+        atk.topk_beam(x, s, 2 ** 32 + 2, stream=torch.cuda.current_stream())
+
+
 def test_the_extension_module_leaves_unusual_calls_alone(lib):
     from approximate_top_selection_b200 import _decode
 
