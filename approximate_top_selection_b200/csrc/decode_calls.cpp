@@ -186,7 +186,9 @@ PyObject* call_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
       usual(PyFloat_Check(a[8]));
       scale = PyFloat_AS_DOUBLE(a[8]);
     }
-    const bool with_lse = a[9] == Py_True;
+    const int truth = PyObject_IsTrue(a[9]);
+    usual(truth >= 0);
+    const bool with_lse = truth != 0;
     const cudaStream_t stream = c10::cuda::getCurrentCUDAStream(dev).stream();
     const at::Tensor ws = workspace(g_lib.attend_bytes(1, 1, 0, static_cast<int>(d)), dev, stream, q);
     at::Tensor out = empty_on(dev, {batch, heads, d}, at::kBFloat16);

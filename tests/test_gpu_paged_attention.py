@@ -348,3 +348,12 @@ def test_two_graphs_replayed_side_by_side():
             assert torch.equal(o[0].view(torch.int16), want[0].view(torch.int16))
             assert torch.equal(o[1].view(torch.int32), want[1].view(torch.int32))
     assert atk.topk_device_status() == 0
+
+
+@pytest.mark.parametrize("asked", [True, 1, False, 0])
+def test_return_lse_by_truth(asked):
+    s = on_gpu(make(1, 2, 1, 64, 8, [9], "bf16", 3))
+    args = (s["q"], s["k_cache"], s["v_cache"], s["table"], s["lens"])
+    for kw in ({}, {"stream": torch.cuda.current_stream()}):
+        got = atk.paged_attention(*args, return_lse=asked, **kw)
+        assert isinstance(got, tuple) == bool(asked)
