@@ -260,7 +260,8 @@ int paged_attention(const uint16_t* q, int64_t q_stride, int64_t batch, int head
   if ((rc = table_view(block_table, table_stride, table_width, seq_lens, batch, k_cache->page_size, &a.tab)))
     return rc;
   if (heads < 1 || heads % k_cache->kv_heads) return TOPK_EINVAL;
-  if (!std::isfinite(scale)) return TOPK_EINVAL;
+  const float scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
+  if (!std::isfinite(scale_log2)) return TOPK_EINVAL;
   if (!aligned16(q) || !aligned16(out) || q_stride < 0 || q_stride > kMaxElems || q_stride % 8) return TOPK_EINVAL;
   if (positions) {
     if (lists < 1 || c < 1 || lists % k_cache->kv_heads || heads % lists) return TOPK_EINVAL;
@@ -286,7 +287,7 @@ int paged_attention(const uint16_t* q, int64_t q_stride, int64_t batch, int head
   a.heads = heads;
   a.lists = positions ? lists : k_cache->kv_heads;
   a.c = c;
-  a.scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
+  a.scale_log2 = scale_log2;
   a.out = out;
   a.lse = out_lse;
   return TK_BY_CACHE(launch_attend, k_cache->d, a.k.scale != nullptr, a, dev, static_cast<cudaStream_t>(stream));

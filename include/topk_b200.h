@@ -325,6 +325,7 @@ int cache_read(const topk_cache *cache, const int32_t *block_table_dev, int64_t 
  *                 one at or behind seq_lens[b] is left out (at or behind
  *                 table_width * page_size it also sets TOPK_DEV_BAD_INDEX);
  *                 a position listed twice counts twice.
+ *   scale         scale * log2(e) finite in float32 (else TOPK_EINVAL).
  *   out_dev       [batch x heads x d] bf16; out_lse_dev NULL or [batch x
  *                 heads] float32.
  * A head with no token to attend to, or whose scores are all -inf, gives

@@ -66,6 +66,11 @@ def test_attention(lib, bad, status):
     assert attend(lib, **bad) == status
 
 
+@pytest.mark.parametrize("scale", [float("inf"), float("nan"), 3e38, -3e38])
+def test_attention_refuses_a_scale_without_log2(lib, scale):
+    assert attend(lib, scale=scale) == E
+
+
 def test_attention_refuses_unlike_caches(lib):
     for other in (dict(pages=5), dict(kv_heads=4), dict(page_size=8), dict(d=64), dict(type=1, scale=P)):
         assert attend(lib, v=cache(**other)) == E
