@@ -39,29 +39,38 @@ __device__ __forceinline__ bool ranks_above(const Cont& a, const Cont& b) {
   return a.token < b.token;
 }
 
-// Two kernels.  A CTA of the first takes a piece of a beam's row, at most 64 KB
-// that stay in its registers: the piece's maximum, its sum of exponentials and
-// its k largest logits.  A CTA of the second, started as the first drains,
-// turns a sentence's sums into lse_i and picks the k best of all pieces' lists.
-// Within a beam the order is the logits', so a piece's list can be cut at k
-// before lse_i is known.  (Leaving the second part to the CTA that finishes a
-// sentence last costs every CTA a fence and an atomic, 1.1 of its 7 us.)
+// Two kernels.  A CTA of the first takes a piece of a beam's row: the piece's
+// maximum, its sum of exponentials and its k largest logits.  A CTA of the
+// second, started as the first drains, turns a sentence's sums into lse_i and
+// picks the k best of all pieces' lists.  Within a beam the order is the
+// logits', so a piece's list can be cut at k before lse_i is known.  (Leaving
+// the second part to the CTA that finishes a sentence last costs every CTA a
+// fence and an atomic, 1.1 of its 7 us.)
 //
 // The k largest of a piece without sorting it: of the 256 threads' maxima, the
 // j-th largest of each warp (j = ceil(k / 8)) bounds the k-th largest value
 // from below in all; the few vectors that reach the smallest of these bounds
-// are set aside while the exponentials are summed, their elements gathered and
-// ranked by counting.  Where that leaves too many (equal logits), the bound is
-// bisected, over keys and then over indices.
+// are set aside, their elements gathered and ranked by counting.  Where that
+// leaves too many (equal logits), the bound is bisected, over keys and then over
+// indices.
+//
+// The first kernel has two forms.  Few rows (a round of CTAs at most): pieces of
+// at most 64 KB that stay in the CTA's registers, the maximum first, then the
+// exponentials relative to it.  Many rows: pieces of up to 256 KB that pass
+// through the registers once, in batches, with a running reference; the few
+// batches that hold candidates are read again, from a cache.  A piece's start
+// and end take about as long as 64 KB of logits, so fewer pieces pay.
 //
 // Bound by reading the logits.  A logit costs one exponential (16 per clock
 // and SM: 4.5e12 a second, against 1.6e12 fp32 or 3.2e12 bf16 logits a second
 // at full bandwidth) and about five other instructions.  Measured: 4 x 131072
-// fp32, k 8: 8.4 us; 32 sentences x 8 x 128255 bf16, k 16: 29.6 us, 2.2 TB/s:
-// 3.5 rounds of CTAs of 6 us, of which 2 wait for the logits, 2 work on them and
-// 2 are the bound, the ranking and the end, with little in flight.  Rejected:
-// resident CTAs with the next piece on its way into shared memory (39 us by
-// cp.async, 38 us by bulk copies: the pieces fit half as many warps).
+// fp32, k 8: 8.4 us (held); 32 sentences x 8 x 128255 bf16, k 16: 25.5 us, 2.6
+// TB/s (streaming; 29.6 held, in 3.5 rounds of CTAs); 512 x 128255 fp32, k 8:
+// 54 us, 4.9 TB/s (67 held).  About 5 us of these are the second kernel.
+// Rejected: resident CTAs with the next held piece on its way into shared memory
+// (39 us by cp.async, 38 us by bulk copies: the pieces fit half as many warps);
+// batches of 8 vectors by two CTAs per SM instead of 4 by four (equal there, a
+// quarter slower on 1024 rows of 32000).
 
 // A piece's largest key (0: nothing) and its sum of 2^(x L - r), with L = log2 e
 // rounded to fp32 and r a whole number near max * L (so that sums join by exact
@@ -90,8 +99,11 @@ struct BeamArgs {
 
 constexpr int kMaxBeams = 128;
 constexpr int kBeamCap = 512;       // gathered candidates; more than the largest k
-constexpr int kBeamHits = 384;      // vectors that hold them
-constexpr int kBeamVectors = 16;    // 16-byte vectors per thread
+constexpr int kBeamHits = 384;      // vectors that hold them, or batches
+constexpr int kBeamBatch = 4;       // 16-byte vectors that a thread takes at a time
+constexpr int kBeamBatches = 16;    // of a thread
+constexpr int kBeamCtasPerSm = 4;
+constexpr int kBeamVectors = 16;    // of a thread, where a piece stays in registers
 
 // Order key of a candidate logit; 0 for one that gives no continuation.
 __device__ __forceinline__ uint32_t beam_key(float x) {
@@ -148,11 +160,12 @@ struct BeamShared {
   };
   uint4 hit[kBeamHits];   // vectors of a piece that reach its bound
   int hit_at[kBeamHits];  // index of their first element
+  int batch[kBeamHits];   // batches that reach it: number * threads + thread
   double off[kMaxBeams];
   double part[kBeamThreads / 32];
   Cont best[kBeamThreads / 32];
   uint32_t warp_keys[kBeamThreads / 32], warp_tops[kBeamThreads / 32];
-  int count, hits, total;
+  int count, hits, batches, total;
 };
 
 __device__ __forceinline__ float exp2_ftz(float x) {
@@ -176,19 +189,20 @@ struct BeamPiece {
 
   __device__ __forceinline__ BeamPiece(const T* row_, int64_t n_, int piece, int pieces) : row(row_), n(n_) {
     mis = static_cast<int>((reinterpret_cast<uintptr_t>(row) / sizeof(T)) % kPer);
-    const int64_t vectors = (n + mis + kPer - 1) / kPer;
-    w0 = vectors * piece / pieces;
-    w1 = vectors * (piece + 1) / pieces;
+    const uint32_t vectors = static_cast<uint32_t>((n + mis + kPer - 1) / kPer);  // n < 2^31
+    const uint32_t each = vectors / static_cast<uint32_t>(pieces), more = vectors - each * pieces;
+    w0 = piece * each + min(static_cast<uint32_t>(piece), more);
+    w1 = w0 + each + (piece < more);
     low = first_ragged() >= 0;
     count = static_cast<int>(w1 - w0) - low - (last_ragged() >= 0);
   }
   __device__ __forceinline__ int64_t vector(int v) const { return w0 + v * kBeamThreads + threadIdx.x; }
   __device__ __forceinline__ int64_t index(int v) const { return vector(v) * kPer - mis; }
   __device__ __forceinline__ bool inside(int64_t w) const { return w * kPer >= mis && (w + 1) * kPer - mis <= n; }
-  // A vector inside the row; what is ragged reads as -inf.
-  __device__ __forceinline__ uint4 load(int v) const {
+  // Vector i of the piece, if it lies inside the row; what is ragged reads as -inf.
+  __device__ __forceinline__ uint4 load(int v) const { return load_at(v * kBeamThreads + static_cast<int>(threadIdx.x)); }
+  __device__ __forceinline__ uint4 load_at(int i) const {
     uint4 x = make_uint4(kFill, kFill, kFill, kFill);
-    const int i = v * kBeamThreads + static_cast<int>(threadIdx.x);
     if (static_cast<unsigned>(i - low) < static_cast<unsigned>(count))
       x = __ldg(reinterpret_cast<const uint4*>(row - mis + w0 * kPer) + i);
     return x;
@@ -262,12 +276,19 @@ __device__ __noinline__ void beam_bisect(BeamShared* shp, const T* row, int64_t 
   BeamShared& sh = *shp;
   const BeamPiece<T> p(row, n, piece, pieces);
   auto each = [&](auto&& f) {
+    const int vectors = static_cast<int>((p.w1 - p.w0 + kBeamThreads - 1) / kBeamThreads);
 #pragma unroll 1
-    for (int v = 0; v < kBeamVectors; ++v) {
-      const int64_t w = p.vector(v);
-      const uint4 x = w < p.w1 && !p.inside(w) ? p.load_ragged(w) : p.load(v);
+    for (int v0 = 0; v0 < vectors; v0 += 4) {
+      uint4 x[4];
 #pragma unroll
-      for (int e = 0; e < p.kPer; ++e) f(beam_key(p.value(x, e)), p.index(v) + e);
+      for (int v = 0; v < 4; ++v) {
+        const int64_t w = p.vector(v0 + v);
+        x[v] = w < p.w1 && !p.inside(w) ? p.load_ragged(w) : p.load(v0 + v);
+      }
+#pragma unroll
+      for (int v = 0; v < 4; ++v)
+#pragma unroll
+        for (int e = 0; e < p.kPer; ++e) f(beam_key(p.value(x[v], e)), p.index(v0 + v) + e);
     }
   };
   uint32_t lo = 1, hi = 0xffffffffu;
@@ -474,22 +495,54 @@ __global__ void __launch_bounds__(kBeamThreads) beam_finish_kernel(BeamArgs p) {
   }
 }
 
-// Grid: sentence-major, then beam, then piece.
+// The elements of the vectors set aside that reach the bound.  All threads.
 template <typename T>
-__global__ void __launch_bounds__(kBeamThreads, 2) topk_beam_kernel(BeamArgs p) {
+__device__ __forceinline__ void beam_gather(BeamShared& sh, uint32_t bound) {
+  constexpr int kPer = BeamPiece<T>::kPer;
+  const int n = min(sh.hits, kBeamHits) * kPer;
+  for (int i = threadIdx.x; i < n; i += kBeamThreads) {
+    const uint32_t key = beam_key(logit_value(reinterpret_cast<const T*>(sh.hit)[i]));
+    if (key >= bound) beam_push(sh, key, sh.hit_at[i / kPer] + i % kPer);
+  }
+}
+
+// The piece's list (its k best of those gathered) and sum.  All threads.
+__device__ __forceinline__ void beam_piece_end(const BeamShared& sh, const BeamArgs& p, uint32_t top, int r) {
+  uint64_t* list = p.lists + static_cast<int64_t>(blockIdx.x) * p.k;
+  const int found = sh.count;
+  beam_rank(
+      found, [&](int j, int i) { return sh.gathered[j] > sh.gathered[i]; },
+      [&](int i, int above) {
+        if (above < p.k) list[above] = sh.gathered[i];
+      });
+  for (int i = found + static_cast<int>(threadIdx.x); i < p.k; i += kBeamThreads) list[i] = 0;
+  if (threadIdx.x == 0) {
+    double t = 0.0;
+#pragma unroll
+    for (int w = 0; w < kBeamThreads / 32; ++w) t += sh.part[w];
+    p.sums[blockIdx.x] = BeamSum{t, top, r};
+  }
+}
+
+// The piece of a beam that has ended.
+__device__ __forceinline__ void beam_piece_ended(const BeamArgs& p) {
+  if (threadIdx.x == 0) p.sums[blockIdx.x] = BeamSum{0.0, 0u, 0};
+  for (int i = threadIdx.x; i < p.k; i += kBeamThreads) p.lists[static_cast<int64_t>(blockIdx.x) * p.k + i] = 0;
+}
+
+// Grid of both kernels: sentence-major, then beam, then piece.
+template <typename T>
+__global__ void __launch_bounds__(kBeamThreads, 2) topk_beam_held_kernel(BeamArgs p) {
   constexpr int kPer = BeamPiece<T>::kPer;
   __shared__ BeamShared sh;
   pdl_wait_then_release();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int64_t row = blockIdx.x / p.pieces;  // of the launch
+  const uint32_t row = blockIdx.x / static_cast<uint32_t>(p.pieces);  // of the launch
   const int piece = static_cast<int>(blockIdx.x - row * p.pieces);
-  BeamSum* sum_out = p.sums + blockIdx.x;
-  uint64_t* list = p.lists + static_cast<int64_t>(blockIdx.x) * p.k;
   const float ninf = __int_as_float(0xff800000);
   if (tid == 0) sh.count = sh.hits = 0;
   if (__ldg(p.scores + p.first * p.beams + row) == ninf) {
-    if (tid == 0) *sum_out = BeamSum{0.0, 0u, 0};
-    for (int i = tid; i < p.k; i += kBeamThreads) list[i] = 0;
+    beam_piece_ended(p);
   } else {
     const T* row_x = static_cast<const T*>(p.logits) + (p.first * p.beams + row) * p.n;
     const BeamPiece<T> pc(row_x, p.n, piece, p.pieces);
@@ -554,11 +607,7 @@ __global__ void __launch_bounds__(kBeamThreads, 2) topk_beam_kernel(BeamArgs p) 
         if (any(v)) add(x[v], pc.index(v));
       if (edge_at >= 0) add(edge, edge_at * kPer - pc.mis);
       __syncthreads();
-      const int hits = min(sh.hits, kBeamHits);
-      for (int i = tid; i < hits * kPer; i += kBeamThreads) {
-        const uint32_t key = beam_key(logit_value(reinterpret_cast<const T*>(sh.hit)[i]));
-        if (key >= bound) beam_push(sh, key, sh.hit_at[i / kPer] + i % kPer);
-      }
+      beam_gather<T>(sh, bound);
     }
     float s = (sum[0] + sum[1]) + (sum[2] + sum[3]);
 #pragma unroll
@@ -566,20 +615,184 @@ __global__ void __launch_bounds__(kBeamThreads, 2) topk_beam_kernel(BeamArgs p) 
     if (lane == 0) sh.part[warp] = s;
     __syncthreads();
     if (key_top && (!gathered || sh.hits > kBeamHits || sh.count > kBeamCap)) beam_bisect(&sh, row_x, p.n, piece, p.pieces, p.k);
-    const int found = sh.count;
-    beam_rank(
-        found, [&](int j, int i) { return sh.gathered[j] > sh.gathered[i]; },
-        [&](int i, int above) {
-          if (above < p.k) list[above] = sh.gathered[i];
-        });
-    for (int i = found + tid; i < p.k; i += kBeamThreads) list[i] = 0;
-    if (tid == 0) {
-      double t = 0.0;
-#pragma unroll
-      for (int w = 0; w < kBeamThreads / 32; ++w) t += sh.part[w];
-      *sum_out = BeamSum{t, key_top, r};
-    }
+    beam_piece_end(sh, p, key_top, r);
   }
+}
+
+// sum * 2^d for a whole number d <= 0; nothing is left below 2^-126, not of an
+// infinite sum either (of logits so large that x L - r is a rounding error).  A
+// larger d is that of an empty sum.
+__device__ __forceinline__ float beam_shrink(float sum, float d) {
+  return d >= -126.0f && d <= 0.0f ? sum * __uint_as_float(static_cast<uint32_t>(127 + static_cast<int>(d)) << 23) : 0.0f;
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kBeamThreads, kBeamCtasPerSm) topk_beam_stream_kernel(BeamArgs p) {
+  using Piece = BeamPiece<T>;
+  constexpr int kPer = Piece::kPer;
+  __shared__ BeamShared sh;
+  __shared__ float batch_top[kBeamBatches * kBeamThreads];  // a thread's own
+  pdl_wait_then_release();
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const uint32_t row = blockIdx.x / static_cast<uint32_t>(p.pieces);  // of the launch
+  const int piece = static_cast<int>(blockIdx.x - row * p.pieces);
+  const float ninf = __int_as_float(0xff800000);
+  if (tid == 0) sh.count = sh.hits = sh.batches = 0;
+  const float score = __ldg(p.scores + p.first * p.beams + row);
+  const T* row_x = static_cast<const T*>(p.logits) + (p.first * p.beams + row) * p.n;
+  const Piece pc(row_x, p.n, piece, p.pieces);
+  // The row's ragged first and last vector go to threads 0 and 32.
+  uint4 edge = make_uint4(pc.kFill, pc.kFill, pc.kFill, pc.kFill);
+  const int64_t edge_at = tid == 0 ? pc.first_ragged() : tid == 32 ? pc.last_ragged() : -1;
+  if (edge_at >= 0) edge = pc.load_ragged(edge_at);
+
+  // One pass: the thread's largest element (NaN counts as the largest), that of
+  // each batch, and the sum of 2^(x L - r).  L's rounding moves the exponent of
+  // a term by 2^-26 of x log2 e, of which the part common to all terms is taken
+  // out at the end.  r is the whole number near the largest x L of the batch that
+  // last passed `lift`, one logit above the one before: exponents stay below 2.
+  float top = ninf, sum = 0.0f, rf = 0.0f, lift = ninf;
+  auto raise = [&](float largest) {
+    top = fmax_nan(top, largest);
+    if (largest > lift) {
+      const float to = rintf(largest * kBeamLog2e);
+      sum = beam_shrink(sum, rf - to);
+      rf = to;
+      lift = largest + 1.0f;
+    }
+  };
+  auto add = [&](float (&part)[4], const uint4& z) {
+#pragma unroll
+    for (int e = 0; e < kPer; ++e) part[e & 3] += exp2_ftz(fmaf(pc.value(z, e), kBeamLog2e, -rf));
+  };
+  const int live = pc.low + pc.count;
+  const int batches = (live + kBeamBatch * kBeamThreads - 1) / (kBeamBatch * kBeamThreads);
+  auto load = [&](uint4 (&x)[kBeamBatch], int b) {
+    const int i0 = b * kBeamBatch * kBeamThreads;
+    if (i0 >= pc.low && i0 + kBeamBatch * kBeamThreads <= live) {
+      const uint4* src = reinterpret_cast<const uint4*>(row_x - pc.mis + pc.w0 * kPer) + i0 + tid;
+#pragma unroll
+      for (int v = 0; v < kBeamBatch; ++v) x[v] = __ldg(src + v * kBeamThreads);
+    } else {
+#pragma unroll
+      for (int v = 0; v < kBeamBatch; ++v) x[v] = pc.load(b * kBeamBatch + v);
+    }
+  };
+  auto take = [&](const uint4 (&x)[kBeamBatch], int b) {
+    uint4 y = x[0];
+#pragma unroll
+    for (int v = 1; v < kBeamBatch; ++v) y = pc.larger(y, x[v]);
+    const float largest = pc.largest(y);
+    batch_top[b * kBeamThreads + tid] = largest;
+    raise(largest);
+    float part[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int v = 0; v < kBeamBatch; ++v)
+      if ((b * kBeamBatch + v) * kBeamThreads < live) add(part, x[v]);
+    sum += (part[0] + part[1]) + (part[2] + part[3]);
+  };
+  uint4 x[kBeamBatch], z[kBeamBatch];
+  load(x, 0);  // not waiting for the score
+  if (score == ninf) {
+    beam_piece_ended(p);
+    return;
+  }
+#pragma unroll 1
+  for (int b = 0; b < batches; b += 2) {
+    load(z, b + 1);
+    take(x, b);
+    if (b + 1 >= batches) break;
+    load(x, b + 2);
+    take(z, b + 1);
+  }
+  if (edge_at >= 0) {
+    float part[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    raise(pc.largest(edge));
+    add(part, edge);
+    sum += (part[0] + part[1]) + (part[2] + part[3]);
+  }
+
+  const uint32_t mine = beam_key(top);
+  const uint32_t warp_top = __reduce_max_sync(0xffffffffu, mine);
+  if (lane == 0) sh.warp_tops[warp] = warp_top;
+  uint32_t bound = max(beam_bound(mine, p.k, sh.warp_keys), 1u);
+  uint32_t key_top = 0;  // the piece's maximum
+#pragma unroll
+  for (int w = 0; w < kBeamThreads / 32; ++w) key_top = max(key_top, sh.warp_tops[w]);
+  int r = 0;
+  const float m = key_top ? key_value(key_top) : 0.0f;
+  if (key_top >= 0xff800000u) {  // a NaN or +inf: no sum
+    sum = 0.0f;
+  } else if (fabsf(m) > 1e6f) {  // x L would be off by more than a fraction of 1
+    r = kBeamByMax;
+    float part[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 1
+    for (int v = 0; v <= batches * kBeamBatch; ++v) {
+      const uint4 y = v < batches * kBeamBatch ? pc.load(v) : edge;
+#pragma unroll
+      for (int e = 0; e < kPer; ++e) part[e & 3] += exp2_ftz((pc.value(y, e) - m) * kBeamLog2e);
+    }
+    sum = (part[0] + part[1]) + (part[2] + part[3]);
+  } else {
+    const float to = rintf(m * kBeamLog2e);
+    r = static_cast<int>(to);
+    sum = beam_shrink(sum, rf - to);
+  }
+#pragma unroll
+  for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  if (lane == 0) sh.part[warp] = sum;
+
+  // Vectors that reach the bound are set aside, from batches that do, which are
+  // read again by a thread per vector (a piece's only batch is still there).
+  auto set_aside = [&](const uint4& y, int64_t i) {
+    if (beam_key(pc.largest(y)) < bound) return;
+    const int at = atomicAdd(&sh.hits, 1);
+    if (at >= kBeamHits) return;
+    sh.hit[at] = y;
+    sh.hit_at[at] = static_cast<int>(i);
+  };
+  bool over;
+  for (bool again = false;; again = true) {
+    if (mine >= bound) {
+      if (batches <= 1) {
+#pragma unroll
+        for (int v = 0; v < kBeamBatch; ++v) set_aside(x[v], pc.index(v));
+      } else {
+        for (int b = 0; b < batches; ++b)
+          if (beam_key(batch_top[b * kBeamThreads + tid]) >= bound) {
+            const int at = atomicAdd(&sh.batches, 1);
+            if (at < kBeamHits) sh.batch[at] = b * kBeamThreads + tid;
+          }
+      }
+      if (edge_at >= 0) set_aside(edge, edge_at * kPer - pc.mis);
+    }
+    __syncthreads();
+    if (batches > 1) {
+      const int n = min(sh.batches, kBeamHits) * kBeamBatch;
+      for (int i = tid; i < n; i += kBeamThreads) {
+        const int batch = sh.batch[i / kBeamBatch];
+        const int at = (batch / kBeamThreads * kBeamBatch + i % kBeamBatch) * kBeamThreads + batch % kBeamThreads;
+        set_aside(pc.load_at(at), (pc.w0 + at) * kPer - pc.mis);
+      }
+      __syncthreads();
+    }
+    beam_gather<T>(sh, bound);
+    __syncthreads();
+    over = sh.batches > kBeamHits || sh.hits > kBeamHits || sh.count > kBeamCap;
+    if (again || !over) break;
+    // Too many (logits in falling order, say): the k-th largest of the threads'
+    // maxima itself, to 16 bits.
+    uint32_t tight = 0;
+    for (int bit = 31; bit >= 16; --bit) {
+      const uint32_t trial = tight | (1u << bit);
+      if (__syncthreads_count(mine >= trial) >= p.k) tight = trial;
+    }
+    bound = max(bound, tight);
+    if (tid == 0) sh.count = sh.hits = sh.batches = 0;
+    __syncthreads();
+  }
+  if (over) beam_bisect(&sh, row_x, p.n, piece, p.pieces, p.k);
+  beam_piece_end(sh, p, key_top, r);
 }
 
 // ---------------------------------------------------------------- reordering

@@ -172,18 +172,43 @@ int launch_read(const ReadArgs& a, const DeviceInfo& dev, cudaStream_t st) {
    : (d) == 128 ? ((e4m3) ? fn<128, true>(__VA_ARGS__) : fn<128, false>(__VA_ARGS__)) \
                 : ((e4m3) ? fn<256, true>(__VA_ARGS__) : fn<256, false>(__VA_ARGS__)))
 
-// Pieces of a beam's row: what the registers of a CTA hold at most, and down
-// to a quarter of that while the pieces are fewer than two per SM.
-int beam_pieces(int64_t rows, int64_t n, int esz, const DeviceInfo& dev) {
+// How a beam's row is cut into pieces.  Where one round of CTAs can hold all
+// rows in registers: into what a CTA holds at most, and down to a quarter of
+// that while the pieces are fewer than two per SM.  Else for the streaming
+// kernel, which has fewer starts and ends to pay for: so many that the rounds
+// of CTAs take the least time, the end of a piece counted as 32 KB of reading.
+// Measured, held and streaming, us, k 8: 64 rows of 128255 bf16 (256 pieces)
+// 11.9, 12.9; fp32 (512) 15.3, 14.4; 192 rows of 32000 fp32 (384) 13.5, 13.1; 512
+// rows of 128255 bf16 44.5, 38.2; fp32 67.2, 53.7; 4 rows of 131072 fp32 9.1, 9.2.
+struct BeamCut {
+  int pieces;
+  bool held;
+};
+BeamCut beam_cut(int64_t rows, int64_t n, int esz, const DeviceInfo& dev) {
   const int64_t vectors = n / (16 / esz) + 2;
-  const int64_t most = static_cast<int64_t>(kBeamThreads) * kBeamVectors;
-  const int64_t least = (vectors + most - 1) / most;
-  const int64_t wanted = std::min(2 * dev.sms / std::max<int64_t>(rows, 1), 4 * vectors / most);
-  return static_cast<int>(std::max(least, wanted));
+  const int64_t held_most = static_cast<int64_t>(kBeamThreads) * kBeamVectors;
+  const int64_t held_least = (vectors + held_most - 1) / held_most;
+  if (rows * held_least <= 2 * dev.sms) {
+    const int64_t wanted = std::min(2 * dev.sms / rows, 4 * vectors / held_most);
+    return {static_cast<int>(std::max(held_least, wanted)), true};
+  }
+  const int64_t most = static_cast<int64_t>(kBeamThreads) * kBeamBatch * kBeamBatches, slots = kBeamCtasPerSm * dev.sms;
+  const int64_t least = (vectors + most - 1) / most, cap = std::max(least, vectors / 1024);
+  int64_t best = 0, best_cost = 0;
+  for (int rounds = 0; rounds <= 4; ++rounds) {  // the most pieces of so many rounds; 0: the fewest pieces
+    const int64_t p = std::min(cap, std::max(least, rounds * slots / rows));
+    const int64_t cost = ((rows * p + slots - 1) / slots) * (vectors / p + 2048);
+    if (best == 0 || cost < best_cost) {
+      best = p;
+      best_cost = cost;
+    }
+  }
+  return {static_cast<int>(best), false};
 }
 
 struct BeamPlan {
   int pieces;
+  bool held;
   int64_t sentences;  // per launch
   size_t sums, lists; // bytes
   size_t total() const { return kTicketBytes + sums + lists; }
@@ -191,7 +216,9 @@ struct BeamPlan {
 
 BeamPlan plan_beam(int64_t batch, int beams, int64_t n, int k, int esz, const DeviceInfo& dev) {
   BeamPlan pl;
-  pl.pieces = beam_pieces(batch * beams, n, esz, dev);
+  const BeamCut cut = beam_cut(batch * beams, n, esz, dev);
+  pl.pieces = cut.pieces;
+  pl.held = cut.held;
   // as many sentences as fit a grid and about 1 GB of lists
   const int64_t sentence_bytes = static_cast<int64_t>(pl.pieces) * (sizeof(BeamSum) + 8 * k) * beams;
   const int64_t fit = std::min<int64_t>((int64_t{1} << 30) / sentence_bytes,
@@ -223,9 +250,10 @@ int run_beam(const T* logits, const float* scores, int64_t batch, int beams, int
   for (; a.first < batch; a.first += pl.sentences) {
     const int64_t sentences = std::min(pl.sentences, batch - a.first);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    if ((rc = launch_pdl(topk_beam_kernel<T>, dim3(static_cast<unsigned>(sentences * beams * pl.pieces)),
-                         dim3(kBeamThreads), 0, st, a)))
-      return rc;
+    const dim3 grid(static_cast<unsigned>(sentences * beams * pl.pieces));
+    rc = pl.held ? launch_pdl(topk_beam_held_kernel<T>, grid, dim3(kBeamThreads), 0, st, a)
+                 : launch_pdl(topk_beam_stream_kernel<T>, grid, dim3(kBeamThreads), 0, st, a);
+    if (rc) return rc;
     rc = launch_pdl(beam_finish_kernel, dim3(static_cast<unsigned>(sentences)), dim3(kBeamThreads), 0, st, a);
     if (rc) return rc;
   }

@@ -146,6 +146,62 @@ def test_extreme_logits():
     check(x, s, 4, run(x, s, 4))
 
 
+def check_many(x, s, k, rows=320):
+    """As many copies of the sentences as make `rows` rows, the first and the last of them checked."""
+    batch, beams, _ = x.shape
+    copies = -(-rows // (batch * beams))
+    got = run(x.repeat(copies, 1, 1), s.repeat(copies, 1), k)
+    check(x, s, k, [t[:batch] for t in got])
+    check(x, s, k, [t[-batch:] for t in got])
+    return got
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("beams,n,k", [(3, 1, 4), (4, 7, 8), (2, 513, 16), (5, 5001, 10), (8, 33000, 16), (1, 128, 128),
+                                       (3, 70001, 128), (1, 150000, 3)])
+def test_many_rows(dtype, beams, n, k):
+    x, s = make(2, beams, n, dtype, n + k)
+    check_many(x, s, k)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("kind", ["ties", "ascending", "descending", "constant", "one stripe"])
+@pytest.mark.parametrize("n,k", [(5000, 8), (50001, 100)])
+def test_many_rows_of_equal_and_ordered_logits(dtype, kind, n, k):
+    x, s = make(1, 2, n, dtype, 7, kind)
+    check_many(x, s, k)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_many_rows_with_ended_beams_and_undefined_logits(dtype):
+    x, s = make(7, 3, 20001, dtype, 5)
+    s[0, 1:] = NINF
+    s[1] = NINF
+    x[2, 0] = NINF
+    x[2, 1, 3:] = NINF
+    s[2, 2] = NINF
+    x[2, 2, 5] = math.nan
+    x[3, :, ::2] = NINF
+    x[4, 1, 20000] = math.nan
+    x[5, 2, 17] = math.inf
+    x[6, 0, 5], x[6, 1, 4000] = math.nan, math.inf
+    check_many(x, s, 6)
+
+
+def test_many_rows_of_extreme_logits():
+    x, s = make(7, 2, 25000, torch.float32, 8)
+    x[0, 0, 77] = 3e38
+    x[1] *= 1e36
+    x[2] = -3.4e38
+    x[2, 1, 9] = -3.3e38
+    x[3, 0] -= 80000.0
+    x[4] *= 1e-42
+    x[4, 0, 3], x[4, 0, 5] = 0.0, -0.0
+    x[5] = torch.arange(25000) * 0.01      # the running maximum rises all the time
+    x[6, :, :20000] = -1e30                # and here at once, from far below
+    check_many(x, s, 4)
+
+
 def test_misaligned_logits_and_given_outputs():
     for dtype in (torch.float32, torch.bfloat16):
         x, s = make(2, 3, 5001, dtype, 9)
