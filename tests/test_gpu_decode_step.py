@@ -190,3 +190,37 @@ def test_calls_with_everything_given_equal_the_usual_ones():
     atk.cache_write(new, new, k1, v1, slots)
     atk.cache_write(new, new, k2, v2, slots, stream=here)
     assert torch.equal(k1, k2) and torch.equal(v1, v2) and not torch.equal(k1, c[1])
+
+
+def test_many_units_and_rows_captured_and_replayed():
+    """Short sequences by whole warps and a streaming beam step in one graph;
+    other lengths, queries and logits are in place at the second replay."""
+    g = torch.Generator().manual_seed(21)
+    batch, heads, page, width = 160, 8, 16, 3
+    q = torch.randn(batch, heads, 128, generator=g).bfloat16().cuda()
+    k, v = (torch.randn(batch * width, 8, page, 128, generator=g).bfloat16().cuda() for _ in range(2))
+    table = torch.randperm(batch * width, generator=g).view(batch, width).to(torch.int32).cuda()
+    lens = torch.randint(0, page * width + 1, (batch,), generator=g, dtype=torch.int32).cuda()
+    logits, scores = torch.randn(160, 2, 5003, generator=g).cuda(), torch.randn(160, 2, generator=g).cuda()
+
+    def step():
+        return [*atk.paged_attention(q, k, v, table, lens, return_lse=True), *atk.topk_beam(logits, scores, 4)]
+
+    first = step()
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        out = step()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(x, y) for x, y in zip(out, first))
+    q.copy_(q.roll(1, 0))
+    lens.copy_(lens.flip(0))
+    logits.copy_(logits.roll(7, 2))
+    second = step()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(x, y) for x, y in zip(out, second))
+    assert not torch.equal(first[0], second[0]) and not torch.equal(first[4], second[4])
+    assert atk.topk_device_status() == 0
