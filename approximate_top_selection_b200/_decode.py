@@ -173,11 +173,13 @@ def _out(t, shape, dtype, name: str, dev: int):
 _devices = [torch.device("cuda", i) for i in range(64)]
 
 
-# Workspace of paged_attention and topk_beam: one per (device, stream) for
-# calls that run at once; its first part is zero before and after every call,
-# the rest is scratch.  A call under stream capture gets one of its own from
-# the graph's memory instead, so that graphs (which may be replayed on other
-# streams, side by side) share none.
+# Workspace of paged_attention: one per (device, stream) for calls that run at
+# once; its first part is zero before and after every call, the rest is scratch.
+# Host threads may share a stream, and then its workspace: a call is one launch,
+# so theirs follow one another.  (topk_beam is two launches, between which
+# another thread's may come: every call takes scratch of its own.)  A call
+# under stream capture gets one of its own from the graph's memory instead, so
+# that graphs (which may be replayed on other streams, side by side) share none.
 _ws_cache: dict = {}
 _WS_ZERO = 16384  # TOPK_DECODE_TICKET_BYTES
 
@@ -397,7 +399,8 @@ def topk_beam(logits: torch.Tensor, beam_scores: torch.Tensor, k: int, *, out_sc
         out_parent = _out(out_parent, shape, _I32, "out_parent", dev)
         out_token = _out(out_token, shape, _I32, "out_token", dev)
         if ws is None:
-            ws = _workspace(_workspace_bytes(topk_beam_workspace_bytes, batch, beams, n, k), dev, sh)
+            ws = torch.empty(_workspace_bytes(topk_beam_workspace_bytes, batch, beams, n, k), dtype=torch.uint8,
+                             device=_devices[dev])
         lib = load_library()
         fn = lib.topk_beam_bf16 if bf16 else lib.topk_beam
         _check(fn(logits.data_ptr(), beam_scores.data_ptr(), batch, beams, n, k, out_scores.data_ptr(),

@@ -118,10 +118,11 @@ Table table_of(PyObject* table_obj, PyObject* lens_obj, int64_t batch, int dev) 
   return Table{data<int32_t>(t), data<int32_t>(l), t.stride(0), static_cast<int>(t.size(1))};
 }
 
-// One workspace per (device, stream), as _decode.py keeps for its own calls; the
-// caller holds it until its launch, while another thread may put a larger one
-// in its place.  Under stream capture a call gets one from the graph's memory:
-// not usual.
+// The attention's workspace, one per (device, stream), as _decode.py keeps for
+// its own calls (threads may share a stream: a call is one launch, so theirs
+// follow one another).  The caller holds it until its launch, while another
+// thread may put a larger one in its place.  Under stream capture a call gets
+// one from the graph's memory: not usual.
 at::Tensor workspace(size_t bytes, int dev, cudaStream_t stream, const at::Tensor& like) {
   cudaStreamCaptureStatus capture = cudaStreamCaptureStatusNone;
   usual(cudaStreamIsCapturing(stream, &capture) == cudaSuccess && capture == cudaStreamCaptureStatusNone);
@@ -260,7 +261,8 @@ PyObject* call_beam(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const cudaStream_t stream = c10::cuda::getCurrentCUDAStream(dev).stream();
     const size_t bytes = g_lib.beam_bytes(batch, static_cast<int>(beams), len, static_cast<int>(k));
     usual(bytes > 0);
-    const at::Tensor ws = workspace(bytes, dev, stream, x);
+    // Scratch of its own: between the call's launches another thread's may follow on the same stream.
+    const at::Tensor ws = empty_on(dev, {static_cast<int64_t>(bytes)}, at::kByte);
     at::Tensor score = empty_on(dev, {batch, k}, at::kFloat);
     at::Tensor parent = empty_on(dev, {batch, k}, at::kInt);
     at::Tensor token = empty_on(dev, {batch, k}, at::kInt);

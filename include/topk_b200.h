@@ -333,9 +333,10 @@ int cache_read(const topk_cache *cache, const int32_t *block_table_dev, int64_t 
  * The workspace holds paged_attention_workspace_bytes(...) bytes, 16-byte
  * aligned, on the device of the call.  Its first TOPK_DECODE_TICKET_BYTES must
  * be zero before its first use and are zero again after every call; the rest is
- * scratch.  It serves any
- * later call of this operator or of topk_beam (not of the selections above),
- * and calls that overlap on the GPU must not share one. */
+ * scratch.  It serves any later call of this operator or of topk_beam (not of
+ * the selections above).  Calls that overlap on the GPU must not share one, nor
+ * may a call be queued with the workspace of a topk_beam that another host
+ * thread is queueing on the same stream: that is several launches. */
 #define TOPK_DECODE_TICKET_BYTES 16384
 int paged_attention(const uint16_t *q_dev, int64_t q_stride, int64_t batch, int heads,
                     const topk_cache *k_cache, const topk_cache *v_cache,
