@@ -64,9 +64,9 @@ __device__ __forceinline__ bool ranks_above(const Cont& a, const Cont& b) {
 // Bound by reading the logits.  A logit costs one exponential (16 per clock
 // and SM: 4.5e12 a second, against 1.6e12 fp32 or 3.2e12 bf16 logits a second
 // at full bandwidth) and about five other instructions.  Measured: 4 x 131072
-// fp32, k 8: 8.4 us (held); 32 sentences x 8 x 128255 bf16, k 16: 25.5 us, 2.6
-// TB/s (streaming; 29.6 held, in 3.5 rounds of CTAs); 512 x 128255 fp32, k 8:
-// 54 us, 4.9 TB/s (67 held).  About 5 us of these are the second kernel.
+// fp32, k 8: 8.3 us (held); 32 sentences x 8 x 128255 bf16, k 16: 27 us, 2.4
+// TB/s (streaming; 31.9 held, in 3.5 rounds of CTAs); 512 x 128255 fp32, k 8:
+// 60 us, 4.4 TB/s (75 held).  About 5 us of these are the second kernel.
 // Rejected: resident CTAs with the next held piece on its way into shared memory
 // (39 us by cp.async, 38 us by bulk copies: the pieces fit half as many warps);
 // batches of 8 vectors by two CTAs per SM instead of 4 by four (equal there, a
@@ -174,9 +174,32 @@ __device__ __forceinline__ float exp2_ftz(float x) {
   return y;
 }
 
-// The piece of a row that a CTA takes, as 16-byte vectors on 16-byte addresses:
-// vector v of a thread holds the row's elements from index(v) on.  A vector
-// behind the piece, and elements outside the row, read as -inf.
+// 16 bytes from byte s (1 .. 15) on of two neighbouring vectors.
+__device__ __forceinline__ uint4 shift_together(const uint4& a, const uint4& b, int s) {
+  const int w = s >> 2, bits = (s & 3) * 8;
+  const uint32_t x0 = w == 0 ? a.x : w == 1 ? a.y : w == 2 ? a.z : a.w;
+  const uint32_t x1 = w == 0 ? a.y : w == 1 ? a.z : w == 2 ? a.w : b.x;
+  const uint32_t x2 = w == 0 ? a.z : w == 1 ? a.w : w == 2 ? b.x : b.y;
+  const uint32_t x3 = w == 0 ? a.w : w == 1 ? b.x : w == 2 ? b.y : b.z;
+  const uint32_t x4 = w == 0 ? b.x : w == 1 ? b.y : w == 2 ? b.z : b.w;
+  return make_uint4(__funnelshift_r(x0, x1, bits), __funnelshift_r(x1, x2, bits), __funnelshift_r(x2, x3, bits),
+                    __funnelshift_r(x3, x4, bits));
+}
+
+// The piece of a row that a CTA takes, as vectors of 16 bytes counted from the
+// row's start.  Which thread adds which elements in which order, and so every
+// bit of the row's sum, is the same wherever the row lies: beams of equal logits
+// tie.  A warp takes 128 successive vectors at a time, four a lane.  Where the
+// row is off a 16-byte address, a vector lies in two aligned ones: the lane
+// loads the one that holds most of it and has the one or two words of the other
+// from its neighbour.  Rows off such addresses take a tenth longer than rows on
+// them (summed by aligned vectors, in an order that depended on the address, they
+// did not): 512 x 128255 fp32 60 us, bf16 42, against 54 and 38.  Rejected: both
+// aligned vectors loaded by every lane, from L1 the second time (fp32 62 us, bf16
+// 56; the shift chosen word by word instead of by constants: 82, 49).  The
+// row's first vector, its last whole one and the rest behind that may have
+// neighbours in theirs: they are "edges", read by elements, by one thread each.
+// A vector behind the piece, and elements behind the row, read as -inf.
 template <typename T>
 struct BeamPiece {
   static constexpr int kPer = 16 / sizeof(T);  // elements per vector
@@ -184,42 +207,132 @@ struct BeamPiece {
   const T* row;
   int64_t n;
   int64_t w0, w1;  // vectors of the piece
-  int mis;         // elements of the row's first vector that lie before the row
-  int low, count;  // vectors of the piece from w0 + low on that lie inside the row: `count`
+  int mis;         // elements from an aligned address to the row's start
+  int low, live;   // vectors w0 + low .. w0 + live - 1 of the piece are no edges
 
   __device__ __forceinline__ BeamPiece(const T* row_, int64_t n_, int piece, int pieces) : row(row_), n(n_) {
     mis = static_cast<int>((reinterpret_cast<uintptr_t>(row) / sizeof(T)) % kPer);
-    const uint32_t vectors = static_cast<uint32_t>((n + mis + kPer - 1) / kPer);  // n < 2^31
+    const uint32_t vectors = static_cast<uint32_t>((n + kPer - 1) / kPer);  // n < 2^31
     const uint32_t each = vectors / static_cast<uint32_t>(pieces), more = vectors - each * pieces;
     w0 = piece * each + min(static_cast<uint32_t>(piece), more);
     w1 = w0 + each + (piece < more);
-    low = first_ragged() >= 0;
-    count = static_cast<int>(w1 - w0) - low - (last_ragged() >= 0);
+    low = w0 == 0;
+    live = max(low, static_cast<int>(min(w1, last()) - w0));
   }
-  __device__ __forceinline__ int64_t vector(int v) const { return w0 + v * kBeamThreads + threadIdx.x; }
-  __device__ __forceinline__ int64_t index(int v) const { return vector(v) * kPer - mis; }
-  __device__ __forceinline__ bool inside(int64_t w) const { return w * kPer >= mis && (w + 1) * kPer - mis <= n; }
-  // Vector i of the piece, if it lies inside the row; what is ragged reads as -inf.
-  __device__ __forceinline__ uint4 load(int v) const { return load_at(v * kBeamThreads + static_cast<int>(threadIdx.x)); }
-  __device__ __forceinline__ uint4 load_at(int i) const {
-    uint4 x = make_uint4(kFill, kFill, kFill, kFill);
-    if (static_cast<unsigned>(i - low) < static_cast<unsigned>(count))
-      x = __ldg(reinterpret_cast<const uint4*>(row - mis + w0 * kPer) + i);
-    return x;
+  // Vector v (of each four successive ones) of this thread.
+  static __device__ __forceinline__ int at(int v) { return at(v >> 2, v & 3, static_cast<int>(threadIdx.x)); }
+  static __device__ __forceinline__ int at(int four, int v, int thread) {
+    return four * (4 * kBeamThreads) + (thread & ~31) * 4 + v * 32 + (thread & 31);
   }
-  // The row's first and last vector, if this piece holds them and they hold
-  // elements of the row's neighbours too; else -1.  (One that is both is first.)
-  __device__ __forceinline__ int64_t first_ragged() const { return w0 == 0 && w1 > 0 && !inside(0) ? 0 : -1; }
-  __device__ __forceinline__ int64_t last_ragged() const {
-    const int64_t w = (n + mis + kPer - 1) / kPer - 1;
-    return w1 > w && w0 <= w && w > 0 && !inside(w) ? w : -1;
+  __device__ __forceinline__ int64_t index(int i) const { return (w0 + i) * kPer; }  // of vector i's first element
+  __device__ __forceinline__ int64_t last() const { return n / kPer - 1; }           // the row's last whole vector
+  __device__ __forceinline__ bool edge(int64_t w) const { return w == 0 || w >= last(); }
+  // The edge that a thread takes, or -1: the first one thread 0, the last whole
+  // one thread 32 and the rest thread 64, where the piece has them.
+  __device__ __forceinline__ int64_t edge_of(int thread) const {
+    const int64_t w = thread == 0 ? 0 : thread == 32 ? last() : thread == 64 ? last() + 1 : -1;
+    return w >= w0 && w < w1 && (w > 0 || thread == 0) ? w : -1;
   }
-  __device__ __forceinline__ uint4 load_ragged(int64_t w) const {
+  // Vector i by itself.
+  __device__ __forceinline__ uint4 load(int i) const {
+    if (i < low || i >= live) return make_uint4(kFill, kFill, kFill, kFill);
+    const uint4* src = reinterpret_cast<const uint4*>(row - mis + w0 * kPer) + i;
+    const uint4 x = __ldg(src);
+    return mis ? shift_together(x, __ldg(src + 1), mis * static_cast<int>(sizeof(T))) : x;
+  }
+
+  // Four vectors of every lane.  The row's start lies kWord words and 0 or 16
+  // bits behind an aligned address; from kWord = 2 on the second of a vector's
+  // two aligned ones is its own, which is one further on.
+  __device__ __forceinline__ int word() const { return mis * static_cast<int>(sizeof(T)) / 4; }
+  __device__ __forceinline__ const uint4* source() const {
+    return reinterpret_cast<const uint4*>(row - mis + w0 * kPer) + (word() >= 2);
+  }
+  __device__ __forceinline__ bool whole(int four) const {
+    return four * 4 * kBeamThreads >= low && (four + 1) * 4 * kBeamThreads <= live;
+  }
+  // The aligned vectors, and the words that complete the warp's last (first) one,
+  // the same for all lanes (loaded by one of them, in a branch of its own, they
+  // were waited for at the branch's end: 512 x 128255 fp32 90 us).
+  // first: source() + at(0).
+  __device__ __forceinline__ void load_four(uint4 (&x)[4], uint2& rest, const uint4* first, int four) const {
+    const int back = word() >= 2, lane = static_cast<int>(threadIdx.x) & 31;
+    const uint4* src = first + four * (4 * kBeamThreads);
+    const uint2* words = reinterpret_cast<const uint2*>(src - lane + (back ? -1 : 128)) + back;
+    rest = make_uint2(kFill, kFill);
+    if (whole(four)) {
+#pragma unroll
+      for (int v = 0; v < 4; ++v) x[v] = __ldg(src + v * 32);
+      if (mis) rest = __ldg(words);
+    } else {
+      // those beside the first and the last vector too: their words are needed
+      const int from = low < live ? low - back : 0, to = low < live ? live - (back || mis == 0) : -1;
+      const int i0 = at(four, 0, static_cast<int>(threadIdx.x)), i = i0 - lane + (back ? -1 : 128);
+#pragma unroll
+      for (int v = 0; v < 4; ++v)
+        x[v] = i0 + v * 32 >= from && i0 + v * 32 <= to ? __ldg(src + v * 32) : make_uint4(kFill, kFill, kFill, kFill);
+      if (mis && i >= from && i <= to) rest = __ldg(words);
+    }
+  }
+  template <int kWord>
+  static __device__ __forceinline__ uint32_t join(uint32_t a, uint32_t b, int bits) {
+    return sizeof(T) == 4 ? a : __funnelshift_r(a, b, bits);
+  }
+  template <int kWord>
+  __device__ __forceinline__ void join_four(uint4 (&x)[4], const uint2& rest) const {
+    constexpr bool kBack = kWord >= 2;
+    // words of the other aligned vector: its last two, its last, its first or its first two
+    constexpr bool kTwo = kWord == 2 || (kWord == 1 && sizeof(T) == 2);
+    if constexpr (kWord == 0 && sizeof(T) == 4) return;
+    const int lane = threadIdx.x & 31, bits = mis * static_cast<int>(sizeof(T)) % 4 * 8;
+    const int from = kBack ? (lane + 31) & 31 : (lane + 1) & 31;
+    const bool turn = lane == (kBack ? 31 : 0);  // gives a word of the vector behind (before)
+    const bool end = lane == (kBack ? 0 : 31);
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int v = kBack ? 3 - u : u, next = kBack ? max(v - 1, 0) : min(v + 1, 3);
+      uint32_t far = kBack ? (turn ? x[next].w : x[v].w) : (turn ? x[next].x : x[v].x), farther = 0;
+      far = __shfl_sync(0xffffffffu, far, from);
+      if (kTwo) farther = __shfl_sync(0xffffffffu, kBack ? (turn ? x[next].z : x[v].z) : (turn ? x[next].y : x[v].y), from);
+      if (u == 3 && end) {
+        far = kBack ? rest.y : rest.x;
+        farther = kBack ? rest.x : rest.y;
+      }
+      const uint4 o = x[v];
+      if constexpr (kWord == 0)
+        x[v] = make_uint4(join<0>(o.x, o.y, bits), join<0>(o.y, o.z, bits), join<0>(o.z, o.w, bits), join<0>(o.w, far, bits));
+      else if constexpr (kWord == 1)
+        x[v] = make_uint4(join<1>(o.y, o.z, bits), join<1>(o.z, o.w, bits), join<1>(o.w, far, bits),
+                          join<1>(far, farther, bits));
+      else if constexpr (kWord == 2)
+        x[v] = make_uint4(join<2>(farther, far, bits), join<2>(far, o.x, bits), join<2>(o.x, o.y, bits),
+                          join<2>(o.y, o.z, bits));
+      else
+        x[v] = make_uint4(join<3>(far, o.x, bits), join<3>(o.x, o.y, bits), join<3>(o.y, o.z, bits),
+                          join<3>(o.z, o.w, bits));
+    }
+  }
+  // Turns what load_four loaded into the vectors themselves.
+  __device__ __forceinline__ void finish_four(uint4 (&x)[4], const uint2& rest, int four) const {
+    if (mis == 0) return;
+    switch (word()) {
+      case 0: join_four<0>(x, rest); break;
+      case 1: join_four<1>(x, rest); break;
+      case 2: join_four<2>(x, rest); break;
+      default: join_four<3>(x, rest); break;
+    }
+    if (whole(four)) return;
+    const int i0 = at(four, 0, static_cast<int>(threadIdx.x));
+#pragma unroll
+    for (int v = 0; v < 4; ++v)
+      if (i0 + v * 32 < low || i0 + v * 32 >= live) x[v] = make_uint4(kFill, kFill, kFill, kFill);
+  }
+  __device__ __forceinline__ uint4 load_edge(int64_t w) const {
     uint32_t word[4] = {kFill, kFill, kFill, kFill};
 #pragma unroll
     for (int e = 0; e < kPer; ++e) {
-      const int64_t i = w * kPer - mis + e;
-      if (i < 0 || i >= n) continue;
+      const int64_t i = w * kPer + e;
+      if (i >= n) continue;
       if constexpr (sizeof(T) == 4)
         word[e] = __float_as_uint(row[i]);
       else
@@ -276,19 +389,19 @@ __device__ __noinline__ void beam_bisect(BeamShared* shp, const T* row, int64_t 
   BeamShared& sh = *shp;
   const BeamPiece<T> p(row, n, piece, pieces);
   auto each = [&](auto&& f) {
-    const int vectors = static_cast<int>((p.w1 - p.w0 + kBeamThreads - 1) / kBeamThreads);
+    const int vectors = static_cast<int>(p.w1 - p.w0);
 #pragma unroll 1
-    for (int v0 = 0; v0 < vectors; v0 += 4) {
+    for (int i0 = threadIdx.x; i0 < vectors + static_cast<int>(threadIdx.x); i0 += 4 * kBeamThreads) {
       uint4 x[4];
 #pragma unroll
       for (int v = 0; v < 4; ++v) {
-        const int64_t w = p.vector(v0 + v);
-        x[v] = w < p.w1 && !p.inside(w) ? p.load_ragged(w) : p.load(v0 + v);
+        const int i = i0 + v * kBeamThreads;
+        x[v] = i < vectors && p.edge(p.w0 + i) ? p.load_edge(p.w0 + i) : p.load(i);
       }
 #pragma unroll
       for (int v = 0; v < 4; ++v)
 #pragma unroll
-        for (int e = 0; e < p.kPer; ++e) f(beam_key(p.value(x[v], e)), p.index(v0 + v) + e);
+        for (int e = 0; e < p.kPer; ++e) f(beam_key(p.value(x[v], e)), p.index(i0 + v * kBeamThreads) + e);
     }
   };
   uint32_t lo = 1, hi = 0xffffffffu;
@@ -546,20 +659,24 @@ __global__ void __launch_bounds__(kBeamThreads, 2) topk_beam_held_kernel(BeamArg
   } else {
     const T* row_x = static_cast<const T*>(p.logits) + (p.first * p.beams + row) * p.n;
     const BeamPiece<T> pc(row_x, p.n, piece, p.pieces);
-    // (vectors that no thread of the piece has are passed over)
-    auto any = [&](int v) { return v * kBeamThreads < pc.low + pc.count; };
-    uint4 x[kBeamVectors];
+    // (vectors that no lane of the warp has are passed over)
+    auto any = [&](int v) { return pc.at(v / 4, v % 4, tid & ~31) < pc.live; };
+    uint4 x[kBeamVectors / 4][4];
+    uint2 rest[kBeamVectors / 4];
+    const uint4* first = pc.source() + pc.at(0);
 #pragma unroll
-    for (int v = 0; v < kBeamVectors; ++v) x[v] = pc.load(v);
-    // The row's ragged first and last vector go to threads 0 and 32.
+    for (int f = 0; f < kBeamVectors / 4; ++f) pc.load_four(x[f], rest[f], first, f);
     uint4 edge = make_uint4(pc.kFill, pc.kFill, pc.kFill, pc.kFill);
-    const int64_t edge_at = tid == 0 ? pc.first_ragged() : tid == 32 ? pc.last_ragged() : -1;
-    if (edge_at >= 0) edge = pc.load_ragged(edge_at);
+    const int64_t edge_at = pc.edge_of(tid);
+    if (edge_at >= 0) edge = pc.load_edge(edge_at);
+#pragma unroll
+    for (int f = 0; f < kBeamVectors / 4; ++f)
+      if (4 * f * kBeamThreads < pc.live) pc.finish_four(x[f], rest[f], f);
     // largest element of the thread (NaN counts as the largest), and the bound
     uint4 y = edge;
 #pragma unroll
     for (int v = 0; v < kBeamVectors; ++v)
-      if (any(v)) y = pc.larger(y, x[v]);
+      if (any(v)) y = pc.larger(y, x[v / 4][v % 4]);
     const float top = pc.largest(y);
     const uint32_t mine = beam_key(top);
     const uint32_t warp_top = __reduce_max_sync(0xffffffffu, mine);
@@ -582,7 +699,7 @@ __global__ void __launch_bounds__(kBeamThreads, 2) topk_beam_held_kernel(BeamArg
       r = kBeamByMax;
 #pragma unroll 1
       for (int v = 0; v <= kBeamVectors; ++v) {
-        const uint4 z = v < kBeamVectors ? pc.load(v) : edge;
+        const uint4 z = v < kBeamVectors ? pc.load(pc.at(v)) : edge;
 #pragma unroll
         for (int e = 0; e < kPer; ++e) sum[e & 3] += exp2_ftz((pc.value(z, e) - m) * kBeamLog2e);
       }
@@ -604,8 +721,8 @@ __global__ void __launch_bounds__(kBeamThreads, 2) topk_beam_held_kernel(BeamArg
       };
 #pragma unroll
       for (int v = 0; v < kBeamVectors; ++v)
-        if (any(v)) add(x[v], pc.index(v));
-      if (edge_at >= 0) add(edge, edge_at * kPer - pc.mis);
+        if (any(v)) add(x[v / 4][v % 4], pc.index(pc.at(v)));
+      if (edge_at >= 0) add(edge, edge_at * kPer);
       __syncthreads();
       beam_gather<T>(sh, bound);
     }
@@ -634,17 +751,19 @@ __global__ void __launch_bounds__(kBeamThreads, kBeamCtasPerSm) topk_beam_stream
   __shared__ float batch_top[kBeamBatches * kBeamThreads];  // a thread's own
   pdl_wait_then_release();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const uint32_t row = blockIdx.x / static_cast<uint32_t>(p.pieces);  // of the launch
-  const int piece = static_cast<int>(blockIdx.x - row * p.pieces);
   const float ninf = __int_as_float(0xff800000);
   if (tid == 0) sh.count = sh.hits = sh.batches = 0;
-  const float score = __ldg(p.scores + p.first * p.beams + row);
-  const T* row_x = static_cast<const T*>(p.logits) + (p.first * p.beams + row) * p.n;
-  const Piece pc(row_x, p.n, piece, p.pieces);
-  // The row's ragged first and last vector go to threads 0 and 32.
-  uint4 edge = make_uint4(pc.kFill, pc.kFill, pc.kFill, pc.kFill);
-  const int64_t edge_at = tid == 0 ? pc.first_ragged() : tid == 32 ? pc.last_ragged() : -1;
-  if (edge_at >= 0) edge = pc.load_ragged(edge_at);
+  auto piece_of = [&](uint32_t block) {
+    const uint32_t row = block / static_cast<uint32_t>(p.pieces);  // of the launch
+    return Piece(static_cast<const T*>(p.logits) + (p.first * p.beams + row) * p.n, p.n,
+                 static_cast<int>(block - row * p.pieces), p.pieces);
+  };
+  auto edge_of = [&](const Piece& pc) {
+    const int64_t w = pc.edge_of(tid);
+    return w >= 0 ? pc.load_edge(w) : make_uint4(pc.kFill, pc.kFill, pc.kFill, pc.kFill);
+  };
+  const float score = __ldg(p.scores + p.first * p.beams + blockIdx.x / static_cast<uint32_t>(p.pieces));
+  const Piece pass = piece_of(blockIdx.x);
 
   // One pass: the thread's largest element (NaN counts as the largest), that of
   // each batch, and the sum of 2^(x L - r).  L's rounding moves the exponent of
@@ -663,55 +782,54 @@ __global__ void __launch_bounds__(kBeamThreads, kBeamCtasPerSm) topk_beam_stream
   };
   auto add = [&](float (&part)[4], const uint4& z) {
 #pragma unroll
-    for (int e = 0; e < kPer; ++e) part[e & 3] += exp2_ftz(fmaf(pc.value(z, e), kBeamLog2e, -rf));
+    for (int e = 0; e < kPer; ++e) part[e & 3] += exp2_ftz(fmaf(Piece::value(z, e), kBeamLog2e, -rf));
   };
-  const int live = pc.low + pc.count;
-  const int batches = (live + kBeamBatch * kBeamThreads - 1) / (kBeamBatch * kBeamThreads);
-  auto load = [&](uint4 (&x)[kBeamBatch], int b) {
-    const int i0 = b * kBeamBatch * kBeamThreads;
-    if (i0 >= pc.low && i0 + kBeamBatch * kBeamThreads <= live) {
-      const uint4* src = reinterpret_cast<const uint4*>(row_x - pc.mis + pc.w0 * kPer) + i0 + tid;
-#pragma unroll
-      for (int v = 0; v < kBeamBatch; ++v) x[v] = __ldg(src + v * kBeamThreads);
-    } else {
-#pragma unroll
-      for (int v = 0; v < kBeamBatch; ++v) x[v] = pc.load(b * kBeamBatch + v);
-    }
-  };
+  const int batches = (pass.live + kBeamBatch * kBeamThreads - 1) / (kBeamBatch * kBeamThreads);
   auto take = [&](const uint4 (&x)[kBeamBatch], int b) {
     uint4 y = x[0];
 #pragma unroll
-    for (int v = 1; v < kBeamBatch; ++v) y = pc.larger(y, x[v]);
-    const float largest = pc.largest(y);
+    for (int v = 1; v < kBeamBatch; ++v) y = Piece::larger(y, x[v]);
+    const float largest = Piece::largest(y);
     batch_top[b * kBeamThreads + tid] = largest;
     raise(largest);
     float part[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
     for (int v = 0; v < kBeamBatch; ++v)
-      if ((b * kBeamBatch + v) * kBeamThreads < live) add(part, x[v]);
+      if (pass.at(b, v, tid & ~31) < pass.live) add(part, x[v]);
     sum += (part[0] + part[1]) + (part[2] + part[3]);
   };
+  static_assert(kBeamBatch == 4, "a batch is four vectors of a lane");
   uint4 x[kBeamBatch], z[kBeamBatch];
-  load(x, 0);  // not waiting for the score
+  uint2 x_rest, z_rest;
+  const uint4* first = pass.source() + pass.at(0);
+  pass.load_four(x, x_rest, first, 0);  // not waiting for the score
   if (score == ninf) {
     beam_piece_ended(p);
     return;
   }
+  if (pass.edge_of(tid) >= 0) {
+    const uint4 edge = edge_of(pass);
+    float part[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    raise(Piece::largest(edge));
+    add(part, edge);
+    sum = (part[0] + part[1]) + (part[2] + part[3]);
+  }
 #pragma unroll 1
   for (int b = 0; b < batches; b += 2) {
-    load(z, b + 1);
+    pass.load_four(z, z_rest, first, b + 1);
+    pass.finish_four(x, x_rest, b);
     take(x, b);
     if (b + 1 >= batches) break;
-    load(x, b + 2);
+    pass.load_four(x, x_rest, first, b + 2);
+    pass.finish_four(z, z_rest, b + 1);
     take(z, b + 1);
   }
-  if (edge_at >= 0) {
-    float part[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    raise(pc.largest(edge));
-    add(part, edge);
-    sum += (part[0] + part[1]) + (part[2] + part[3]);
-  }
 
+  // The piece once more: what the loop above does not need of it holds no registers there.
+  uint32_t block = blockIdx.x;
+  asm volatile("" : "+r"(block));
+  const Piece pc = piece_of(block);
+  const int64_t edge_at = pc.edge_of(tid);
   const uint32_t mine = beam_key(top);
   const uint32_t warp_top = __reduce_max_sync(0xffffffffu, mine);
   if (lane == 0) sh.warp_tops[warp] = warp_top;
@@ -728,7 +846,7 @@ __global__ void __launch_bounds__(kBeamThreads, kBeamCtasPerSm) topk_beam_stream
     float part[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll 1
     for (int v = 0; v <= batches * kBeamBatch; ++v) {
-      const uint4 y = v < batches * kBeamBatch ? pc.load(v) : edge;
+      const uint4 y = v < batches * kBeamBatch ? pc.load(pc.at(v)) : edge_of(pc);
 #pragma unroll
       for (int e = 0; e < kPer; ++e) part[e & 3] += exp2_ftz((pc.value(y, e) - m) * kBeamLog2e);
     }
@@ -756,7 +874,7 @@ __global__ void __launch_bounds__(kBeamThreads, kBeamCtasPerSm) topk_beam_stream
     if (mine >= bound) {
       if (batches <= 1) {
 #pragma unroll
-        for (int v = 0; v < kBeamBatch; ++v) set_aside(x[v], pc.index(v));
+        for (int v = 0; v < kBeamBatch; ++v) set_aside(x[v], pc.index(pc.at(v)));
       } else {
         for (int b = 0; b < batches; ++b)
           if (beam_key(batch_top[b * kBeamThreads + tid]) >= bound) {
@@ -764,15 +882,15 @@ __global__ void __launch_bounds__(kBeamThreads, kBeamCtasPerSm) topk_beam_stream
             if (at < kBeamHits) sh.batch[at] = b * kBeamThreads + tid;
           }
       }
-      if (edge_at >= 0) set_aside(edge, edge_at * kPer - pc.mis);
+      if (edge_at >= 0) set_aside(edge_of(pc), edge_at * kPer);
     }
     __syncthreads();
     if (batches > 1) {
       const int n = min(sh.batches, kBeamHits) * kBeamBatch;
       for (int i = tid; i < n; i += kBeamThreads) {
         const int batch = sh.batch[i / kBeamBatch];
-        const int at = (batch / kBeamThreads * kBeamBatch + i % kBeamBatch) * kBeamThreads + batch % kBeamThreads;
-        set_aside(pc.load_at(at), (pc.w0 + at) * kPer - pc.mis);
+        const int at = pc.at(batch / kBeamThreads, i % kBeamBatch, batch % kBeamThreads);
+        set_aside(pc.load(at), pc.index(at));
       }
       __syncthreads();
     }
@@ -791,7 +909,7 @@ __global__ void __launch_bounds__(kBeamThreads, kBeamCtasPerSm) topk_beam_stream
     if (tid == 0) sh.count = sh.hits = sh.batches = 0;
     __syncthreads();
   }
-  if (over) beam_bisect(&sh, row_x, p.n, piece, p.pieces, p.k);
+  if (over) beam_bisect(&sh, pc.row, p.n, static_cast<int>(block % static_cast<uint32_t>(p.pieces)), p.pieces, p.k);
   beam_piece_end(sh, p, key_top, r);
 }
 
@@ -824,18 +942,6 @@ struct ReorderArgs {
 __host__ __device__ inline int64_t reorder_items(int64_t rows, int64_t row_bytes) {
   if (row_bytes <= kReorderShort) return (rows + kReorderThreads / 32 - 1) / (kReorderThreads / 32);
   return rows * ((row_bytes + kReorderChunk - 1) / kReorderChunk);
-}
-
-// 16 bytes from byte s (1 .. 15) on of two neighbouring vectors.
-__device__ __forceinline__ uint4 shift_together(const uint4& a, const uint4& b, int s) {
-  const int w = s >> 2, bits = (s & 3) * 8;
-  const uint32_t x0 = w == 0 ? a.x : w == 1 ? a.y : w == 2 ? a.z : a.w;
-  const uint32_t x1 = w == 0 ? a.y : w == 1 ? a.z : w == 2 ? a.w : b.x;
-  const uint32_t x2 = w == 0 ? a.z : w == 1 ? a.w : w == 2 ? b.x : b.y;
-  const uint32_t x3 = w == 0 ? a.w : w == 1 ? b.x : w == 2 ? b.y : b.z;
-  const uint32_t x4 = w == 0 ? b.x : w == 1 ? b.y : w == 2 ? b.z : b.w;
-  return make_uint4(__funnelshift_r(x0, x1, bits), __funnelshift_r(x1, x2, bits), __funnelshift_r(x2, x3, bits),
-                    __funnelshift_r(x3, x4, bits));
 }
 
 // Vectors [v0, v1) of a row's body and, where `edges`, the bytes around the

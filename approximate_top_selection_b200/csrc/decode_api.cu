@@ -178,8 +178,8 @@ int launch_read(const ReadArgs& a, const DeviceInfo& dev, cudaStream_t st) {
 // kernel, which has fewer starts and ends to pay for: so many that the rounds
 // of CTAs take the least time, the end of a piece counted as 32 KB of reading.
 // Measured, held and streaming, us, k 8: 64 rows of 128255 bf16 (256 pieces)
-// 11.9, 12.9; fp32 (512) 15.3, 14.4; 192 rows of 32000 fp32 (384) 13.5, 13.1; 512
-// rows of 128255 bf16 44.5, 38.2; fp32 67.2, 53.7; 4 rows of 131072 fp32 9.1, 9.2.
+// 12.7, 16.1; fp32 (512) 16.6, 16.4; 192 rows of 32000 fp32 (384) 14.1, 14.4; 512
+// rows of 128255 bf16 48.5, 41.7; fp32 74.6, 59.7; 4 rows of 131072 fp32 8.9, 9.1.
 struct BeamCut {
   int pieces;
   bool held;

@@ -361,8 +361,12 @@ size_t paged_attention_workspace_bytes(int64_t batch, int heads, int lists, int 
  *   out_scores_dev  [batch x k] float32 values, best first; out_parent_dev
  *                   [batch x k] int32 beams; out_token_dev [batch x k] int32.
  * Continuations rank by value, compared in 64 bits (NaN first), then by lower
- * beam, larger logit, lower token.  A logit of -inf gives no continuation; a
- * beam whose logits hold a NaN or +inf has the value NaN for all of its own.
+ * beam, larger logit, lower token.  A beam's log-sum-exp is within 2^-18 (n up
+ * to 2^18), and in one call the same for equal logits wherever they lie: beams
+ * of equal logits and scores tie exactly, and only continuations of unlike
+ * beams whose values are within 2^-17 of each other may change places.  A logit
+ * of -inf gives no continuation; a beam whose logits hold a NaN or +inf has the
+ * value NaN for all of its own.
  * When there are fewer than k, the remaining slots hold -inf, -1, -1.
  * Workspace: topk_beam_workspace_bytes(...), shared with paged_attention on
  * the terms given there. */
