@@ -558,8 +558,11 @@ struct AttendWarp {
 #pragma unroll
     for (int k = 0; k < kGroups; ++k) {
       // P^T as the right operand.  Beside bf16 values P is split into two bf16
-      // parts (the second takes what rounding the first left), which keeps 16
-      // bits of every weight.
+      // parts: the upper half of its bits, and what is left, rounded.  That keeps
+      // 16 bits of every weight, and both parts are positive (the last of the 24
+      // bits is set for it, 2^-23 of the weight), so that an infinite value gives
+      // an infinite product with each and not NaN with a second part of zero or
+      // below.
       uint32_t hi[NT][2], lo[NT][2];
 #pragma unroll
       for (int n = 0; n < NT; ++n)
@@ -569,10 +572,10 @@ struct AttendWarp {
           if constexpr (kE4m3) {
             hi[n][y] = transpose8x8(floats_to_f16x2(a, b));
           } else {
-            const uint32_t h = floats_to_bf16x2(a, b);
-            hi[n][y] = transpose8x8(h);
-            lo[n][y] = transpose8x8(
-                floats_to_bf16x2(a - __uint_as_float(h << 16), b - __uint_as_float(h & 0xffff0000u)));
+            const uint32_t x = __float_as_uint(a), z = __float_as_uint(b);
+            hi[n][y] = transpose8x8(__byte_perm(x, z, 0x7632));
+            lo[n][y] = transpose8x8(floats_to_bf16x2(__uint_as_float(x | 1u) - __uint_as_float(x & 0xffff0000u),
+                                                     __uint_as_float(z | 1u) - __uint_as_float(z & 0xffff0000u)));
           }
         }
       if constexpr (kE4m3) {

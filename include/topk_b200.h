@@ -329,7 +329,9 @@ int cache_read(const topk_cache *cache, const int32_t *block_table_dev, int64_t 
  *   out_dev       [batch x heads x d] bf16; out_lse_dev NULL or [batch x
  *                 heads] float32.
  * A head with no token to attend to, or whose scores are all -inf, gives
- * zeros and an lse of -inf.
+ * zeros and an lse of -inf.  An infinite V_j makes its columns infinite (NaN
+ * where infinities of both signs meet, or where p_j is below 2^-100 of the
+ * largest p).
  * The workspace holds paged_attention_workspace_bytes(...) bytes, 16-byte
  * aligned, on the device of the call.  Its first TOPK_DECODE_TICKET_BYTES must
  * be zero before its first use and are zero again after every call; the rest is

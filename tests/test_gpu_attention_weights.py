@@ -1,0 +1,126 @@
+"""Attention where the weights or the values span more than a float's bits.
+
+The bound on an output is the one that test_gpu_paged_attention derives."""
+import math
+
+import pytest
+import torch
+
+import approximate_top_selection_b200 as atk
+
+pytestmark = pytest.mark.gpu
+
+DEV = "cuda:0"
+U = 2.0 ** -24
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    if not torch.cuda.is_available():
+        pytest.fail("these tests need a CUDA device")
+    atk.load_library()
+    torch.cuda.synchronize()
+    atk.topk_device_status()
+    yield
+
+
+def contiguous(batch, heads, kv_heads, d, lens, seed, page=16):
+    """A bf16 case whose sequences own their pages in order."""
+    g = torch.Generator(device=DEV).manual_seed(seed)
+    width = -(-max(lens) // page)
+    s = dict(q=torch.randn(batch, heads, d, generator=g, device=DEV).bfloat16(),
+             table=torch.arange(batch * width, device=DEV, dtype=torch.int32).view(batch, width),
+             lens=torch.tensor(lens, dtype=torch.int32, device=DEV), k_scale=None, v_scale=None)
+    for n in "kv":
+        s[n] = torch.randn(batch * width, kv_heads, page, d, generator=g, device=DEV).bfloat16()
+    return s
+
+
+def call(s, **kw):
+    return atk.paged_attention(s["q"], s["k"], s["v"], s["table"], s["lens"], k_scale=s["k_scale"], v_scale=s["v_scale"],
+                               return_lse=True, **kw)
+
+
+def rows(s, name, b):
+    """Rows [kv_heads, n, d] of sequence b in 64 bits, and their scales (1 for bf16)."""
+    n = int(s["lens"][b])
+    x = s[name][s["table"][b].long()].double()
+    w = s[name + "_scale"]
+    w = torch.ones(x.shape[:3], dtype=torch.float64, device=DEV) if w is None else w[s["table"][b].long()].double()
+    return x.transpose(0, 1).flatten(1, 2)[:, :n], w.transpose(0, 1).flatten(1, 2)[:, :n]
+
+
+def reference(s, scale=None):
+    """(out, tolerance, lse) in 64 bits."""
+    outs, tols, lses = [], [], []
+    batch, heads, d = s["q"].shape
+    scale = d ** -0.5 if scale is None else scale
+    e4m3 = s["k_scale"] is not None
+    for b in range(batch):
+        (k, ks), (v, vs) = rows(s, "k", b), rows(s, "v", b)
+        kv_heads, n, _ = k.shape
+        q = s["q"][b].double().view(kv_heads, -1, d)
+        t = q @ (k * ks[..., None]).transpose(1, 2) * scale
+        size = abs(scale) * q.norm(dim=2)[..., None] * (k * ks[..., None]).norm(dim=2).amax(1).view(-1, 1, 1)
+        p = torch.softmax(t, 2)
+        o, mass = p @ (v * vs[..., None]), p @ (v * vs[..., None]).abs()
+        weights = (2.0 ** -11 if e4m3 else 2.0 ** -16)
+        tol = 2.0 ** -8 * o.abs() + 2.0 ** -134 + (2 * size * (2 * d + 2) * U + 2.0 ** -20 + weights + 2 * U * (n + 64)) * mass
+        outs.append(o.reshape(heads, d))
+        tols.append(tol.reshape(heads, d))
+        lses.append(torch.logsumexp(t, 2).reshape(heads))
+    return torch.stack(outs), torch.stack(tols), torch.stack(lses)
+
+
+def check(s, got=None, **kw):
+    out, lse = got or call(s, **kw)
+    o, tol, l = reference(s, **kw)
+    out = out.double()
+    assert torch.equal(torch.isnan(out), torch.isnan(o))
+    assert torch.equal(torch.isinf(out), torch.isinf(o)) and torch.equal(out[torch.isinf(o)], o[torch.isinf(o)])
+    fine = torch.isfinite(o) & torch.isfinite(tol)
+    assert int(fine.sum()) > 0
+    assert bool(((out - o).abs() <= tol)[fine].all()), float(((out - o).abs() / tol)[fine].max())
+    assert bool(((lse.double() - l).abs() <= 2.0 ** -10 + 2.0 ** -20 * l.abs()).all())
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("batch,heads,kv_heads,longest", [(2, 4, 4, 40), (1, 8, 1, 3000), (3, 12, 1, 500), (40, 16, 16, 47),
+                                                          (2, 40, 2, 333)])
+def test_infinite_values(batch, heads, kv_heads, longest, d):
+    """sum_j p_j V_j is infinite where one V_j is, and undefined only where they disagree."""
+    lens = [max(2, longest - 7 * b) for b in range(batch)]
+    s = contiguous(batch, heads, kv_heads, d, lens, longest + d)
+    for b in range(batch):
+        last = lens[b] - 1
+        at = [(s["table"][b, t // 16].item(), t % 16) for t in (0, 1, last)]
+        s["v"][at[0][0], :, at[0][1], 0:3] = math.inf
+        s["v"][at[1][0], :, at[1][1], 3] = -math.inf
+        s["v"][at[2][0], :, at[2][1], 5:9] = -math.inf
+        s["v"][at[0][0], :, at[0][1], 7] = math.inf     # meets the -inf of the last token
+        s["v"][at[0][0], :, at[0][1], d - 1] = math.nan
+    check(s)
+
+
+def test_infinite_values_of_listed_positions():
+    s = contiguous(2, 8, 8, 128, [300, 200], 3)
+    s["v"][:, :, ::3, ::5] = math.inf
+    pos = torch.arange(200, device=DEV, dtype=torch.int32).expand(2, 8, 200).contiguous()
+    got = call(s, positions=pos)
+    s["lens"] = torch.tensor([200, 200], dtype=torch.int32, device=DEV)
+    check(s, got)
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("heads", [1, 16])
+def test_infinite_values_of_small_weights(heads, d):
+    """Weights that are powers of two, of which a second part would be zero."""
+    s = contiguous(1, heads, 1, d, [200], 7)
+    s["q"][:] = 0
+    s["q"][..., 0] = 1.0
+    s["k"][..., 0] = 0.0
+    for key, score, col in ((0, -1.0, 0), (70, -20.0, 1), (133, -60.0, 2), (199, -98.0, 3)):
+        s["k"][key // 16, 0, key % 16, 0] = score
+        s["v"][key // 16, 0, key % 16, col] = math.inf
+    out, _ = call(s, scale=math.log(2.0))  # scores are powers of two's exponents
+    assert bool((out[..., :4] == math.inf).all()) and bool(torch.isfinite(out[..., 4:]).all())
