@@ -92,12 +92,12 @@ struct AttendShape {
   static constexpr int kStages = D == 64 && kE4m3 ? (kThree ? 3 : 5) : kThree ? 2 : D == 256 && kE4m3 && NT == 2 ? 5 : 3;
   static constexpr int kSlots = 2 * kStages - 1;  // tiles from their tokens to their rows
   static constexpr int kJoinFloats = kThree ? 1280 : 1792;
-  // shared memory: [warps][stages] tiles, join buffer, Q fragments, (m, l) per warp and joined,
+  // shared memory: [warps][stages] tiles, join buffer, Q fragments, (m, l) per warp,
   // [warps][slots] tokens, pages and places, [warps][stages] valid masks, plan
   static constexpr int kOffJoin = kAttendWarps * kStages * kStageBytes;
   static constexpr int kOffQ = kOffJoin + kJoinFloats * 4;
   static constexpr int kOffMl = kOffQ + (kQShared ? 8192 : 0);
-  static constexpr int kOffPlace = kOffMl + (kAttendWarps + 1) * 32 * 4;
+  static constexpr int kOffPlace = kOffMl + kAttendWarps * 32 * 4;
   static constexpr int kOffToken = kOffPlace + kAttendWarps * kSlots * 16;
   static constexpr int kOffPage = kOffToken + kAttendWarps * kSlots * kKeys * 4;
   static constexpr int kOffPlan = kOffPage + kAttendWarps * kSlots * kKeys * 4;
@@ -278,7 +278,7 @@ struct AttendWarp {
 
   float o[NT][D / 16][4];
   float m[NT][2], l[NT][2];
-  float f[NT][2];    // e4m3: O holds sum w_j V8_j / f, with w_j = 2^(s_j - m) * vscale_j
+  float f[NT][2];    // e4m3: O holds sum w_j V8_j / f, with w_j = 2^(s_j - m) * vscale_j; at least kLeast
   float inv[NT][2];  // 1 / f
   uint32_t q[NT][S::kQShared ? 1 : kSteps][kQWords];
   float head_scale[NT][2];  // score in log2 units per unit of the product
@@ -294,13 +294,14 @@ struct AttendWarp {
       for (int h = 0; h < 2; ++h) {
         m[n][h] = __int_as_float(0xff800000);
         l[n][h] = 0.0f;
-        f[n][h] = inv[n][h] = 0.0f;
+        f[n][h] = kLeast;
+        inv[n][h] = 1.0f / kLeast;
       }
     }
   }
 
-  // Weights below 2^-126 count as nothing.
-  static __device__ __forceinline__ float inverse(float f) { return f >= 1.2e-38f ? 1.0f / f : 0.0f; }
+  // The smallest f, whose inverse is finite: the smallest scale, 2^-127, is half of it.
+  static constexpr float kLeast = 1.17549435e-38f;  // 2^-126
 
   static __device__ __forceinline__ int key_of(int r) {
     return kE4m3 ? ((r & 6) << 1) + (r & 1) + ((r >> 2) & 2) : r;
@@ -480,8 +481,16 @@ struct AttendWarp {
           m[n][h] = mn;
           l[n][h] *= x;
           if constexpr (kE4m3) {
-            f[n][h] *= x;
-            inv[n][h] = inverse(f[n][h]);
+            const float fn = f[n][h] * x;
+            f[n][h] = fmaxf(fn, kLeast);
+            inv[n][h] = 1.0f / f[n][h];
+            if (fn < kLeast) {  // what f cannot follow, O does
+#pragma unroll
+              for (int j = 0; j < D / 16; ++j) {
+                o[n][j][h] *= fn * (1.0f / kLeast);
+                o[n][j][2 + h] *= fn * (1.0f / kLeast);
+              }
+            }
           } else {
 #pragma unroll
             for (int j = 0; j < D / 16; ++j) {
@@ -533,10 +542,10 @@ struct AttendWarp {
         for (int n = 0; n < NT; ++n)
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            const float fn = fmaxf(f[n][h], fminf(column_max(wt[n][h]), 1e36f));
-            const float x = fn > 0.0f ? f[n][h] / fn : 0.0f;
+            const float fn = fmaxf(f[n][h], fminf(column_max(wt[n][h]), 8e37f));  // 1 / f is to be no subnormal
+            const float x = f[n][h] / fn;
             f[n][h] = fn;
-            inv[n][h] = inverse(fn);
+            inv[n][h] = 1.0f / fn;
 #pragma unroll
             for (int j = 0; j < D / 16; ++j) {
               o[n][j][h] *= x;
@@ -617,12 +626,12 @@ struct AttendWarp {
       for (int h = 0; h < 2; ++h) {
         const int row = n * 8 + 2 * t + h;
         const float sum = column_sum(l[n][h]);
-        float factor = sum == 0.0f ? 0.0f : 1.0f / sum;
-        if constexpr (kE4m3) factor *= f[n][h];
+        const float factor = sum == 0.0f ? 0.0f : 1.0f / sum;
+        const float unit = kE4m3 ? f[n][h] : 1.0f;  // a factor of its own: f / sum may be a subnormal
         uint16_t* dst = p.out + (out_row + row) * D + (g & 1 ? 7 + g : g);
 #pragma unroll
         for (int j = 0; j < D / 16; ++j) {
-          const float a = o[n][j][h] * factor, b = o[n][j][2 + h] * factor;
+          const float a = o[n][j][h] * factor * unit, b = o[n][j][2 + h] * factor * unit;
           const float c = __shfl_xor_sync(0xffffffffu, g & 1 ? a : b, 4);
           if (row < rows)
             *reinterpret_cast<uint32_t*>(dst + 16 * j) = g & 1 ? floats_to_bf16x2(c, b) : floats_to_bf16x2(a, c);
@@ -637,7 +646,8 @@ struct AttendWarp {
 
 // ---------------------------------------------------------------- joining
 // The part of a unit that CTA c holds: its first CTA writes slot 1, the others
-// (which continue a unit) slot 0.  m of 16 rows, l of 16 rows, O [16][D].
+// (which continue a unit) slot 0.  m of 16 rows, l of 16 rows, O / l [16][D]
+// (means of V, which fit a float whenever V does).
 template <int D>
 __device__ __forceinline__ float* attend_part(float* parts, int c, int first) {
   return parts + static_cast<int64_t>(c * 2 + (c == first)) * attend_part_floats(D);
@@ -651,7 +661,7 @@ template <int D>
 __device__ __noinline__ void attend_join(float* parts, int first, int c0, int n, int step, int rows, bool final,
                                          uint16_t* out, float* lse, float* buf) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  float* weight = buf;        // [rows][32]
+  float* weight = buf;        // [rows][32], the parts' shares of the row
   float* mass = buf + 512;    // [rows] max, [rows] sum
   float* half = buf + 544;    // [<= 128][4] partial sums
   for (int r = warp; r < rows; r += kAttendWarps) {
@@ -665,10 +675,11 @@ __device__ __noinline__ void attend_join(float* parts, int first, int c0, int n,
 #pragma unroll
     for (int x = 16; x; x >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, x));
     const float w = exp2_fast(m - finite_or_zero(mm));
-    float sum = lane < n ? w * l : 0.0f;
+    const float mine = lane < n ? w * l : 0.0f;
+    float sum = mine;
 #pragma unroll
     for (int x = 16; x; x >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
-    weight[r * 32 + lane] = w;
+    weight[r * 32 + lane] = sum == 0.0f ? 0.0f : __fdividef(mine, sum);
     if (lane == 0) {
       mass[r] = mm;
       mass[16 + r] = sum;
@@ -710,9 +721,8 @@ __device__ __noinline__ void attend_join(float* parts, int first, int c0, int n,
     }
     if (i < total && s == 0) {
       if (final) {
-        const float inv = mass[16 + r] == 0.0f ? 0.0f : 1.0f / mass[16 + r];
         *reinterpret_cast<uint2*>(out + r * D + col) =
-            make_uint2(floats_to_bf16x2(acc.x * inv, acc.y * inv), floats_to_bf16x2(acc.z * inv, acc.w * inv));
+            make_uint2(floats_to_bf16x2(acc.x, acc.y), floats_to_bf16x2(acc.z, acc.w));
       } else {
         *reinterpret_cast<float4*>(dst0 + 32 + r * D + col) = acc;  // read by this thread alone
       }
@@ -1085,27 +1095,29 @@ __global__ void __launch_bounds__(kAttendThreads, (AttendShape<D, kE4m3, NT>::kC
         }
       }
     __syncthreads();
+    // m and l of a row of all four warps
+    auto joined = [&](int row, float& mm, float& sum) {
+      mm = ml[row];
+#pragma unroll
+      for (int x = 1; x < kAttendWarps; ++x) mm = fmaxf(mm, ml[x * 32 + row]);
+      sum = 0.0f;
+#pragma unroll
+      for (int x = 0; x < kAttendWarps; ++x) sum += ml[x * 32 + 16 + row] * exp2_fast(ml[x * 32 + row] - finite_or_zero(mm));
+    };
     float factor[NT][2];
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        float mm = w.m[n][h];
-#pragma unroll
-        for (int x = 0; x < kAttendWarps; ++x) mm = fmaxf(mm, ml[x * 32 + n * 8 + 2 * t + h]);
-        factor[n][h] = exp2_fast(w.m[n][h] - finite_or_zero(mm));
-        if constexpr (kE4m3) factor[n][h] *= w.f[n][h];
+        float mm, sum;
+        joined(n * 8 + 2 * t + h, mm, sum);
+        factor[n][h] = sum == 0.0f ? 0.0f : __fdividef(exp2_fast(w.m[n][h] - finite_or_zero(mm)), sum);
       }
     float* part = p.parts + static_cast<int64_t>(blockIdx.x * 2 + (unit_first >= g0)) * attend_part_floats(D);
     const int64_t out_row = static_cast<int64_t>(cur.b) * p.heads + head;
-    float* inverse = ml + kAttendWarps * 32;  // 1 / l of every row, for rows that end here
     if (tid < rows) {
-      float mm = __int_as_float(0xff800000), sum = 0.0f;
-#pragma unroll
-      for (int x = 0; x < kAttendWarps; ++x) mm = fmaxf(mm, ml[x * 32 + tid]);
-#pragma unroll
-      for (int x = 0; x < kAttendWarps; ++x) sum += ml[x * 32 + 16 + tid] * exp2_fast(ml[x * 32 + tid] - finite_or_zero(mm));
-      inverse[tid] = sum == 0.0f ? 0.0f : 1.0f / sum;
+      float mm, sum;
+      joined(tid, mm, sum);
       if (!whole) {
         part[tid] = mm;
         part[16 + tid] = sum;
@@ -1125,7 +1137,8 @@ __global__ void __launch_bounds__(kAttendThreads, (AttendShape<D, kE4m3, NT>::kC
           for (int i = 0; i < 4; ++i) {
             const int head_row = n * 8 + 2 * t + (i & 1);
             if (head_row < rows)
-              join[(warp * rows + head_row) * pitch + W::column(j, i, lane_g) - c0] = w.o[n][j][i] * factor[n][i & 1];
+              join[(warp * rows + head_row) * pitch + W::column(j, i, lane_g) - c0] =
+                  w.o[n][j][i] * factor[n][i & 1] * (kE4m3 ? w.f[n][i & 1] : 1.0f);
           }
       }
       __syncthreads();
@@ -1141,7 +1154,7 @@ __global__ void __launch_bounds__(kAttendThreads, (AttendShape<D, kE4m3, NT>::kC
         }
         if (whole)
           *reinterpret_cast<uint32_t*>(p.out + (out_row + y) * D + c0 + c) =
-              floats_to_bf16x2(v.x * inverse[y], v.y * inverse[y]);
+              floats_to_bf16x2(v.x, v.y);
         else
           *reinterpret_cast<float2*>(part + 32 + y * D + c0 + c) = v;
       }

@@ -331,7 +331,9 @@ int cache_read(const topk_cache *cache, const int32_t *block_table_dev, int64_t 
  * A head with no token to attend to, or whose scores are all -inf, gives
  * zeros and an lse of -inf.  An infinite V_j makes its columns infinite (NaN
  * where infinities of both signs meet, or where p_j is below 2^-100 of the
- * largest p).
+ * largest p).  BF16 values above 2^119 / seq_lens[b] may overflow the sums, in
+ * which weights are relative to a score up to 2^8 below the largest; E4M3 codes
+ * take scales from 2^-127 on, and any whose product with 448 is finite.
  * The workspace holds paged_attention_workspace_bytes(...) bytes, 16-byte
  * aligned, on the device of the call.  Its first TOPK_DECODE_TICKET_BYTES must
  * be zero before its first use and are zero again after every call; the rest is

@@ -1,6 +1,8 @@
 """Attention where the weights or the values span more than a float's bits.
 
-The bound on an output is the one that test_gpu_paged_attention derives."""
+The bound on an output is the one that test_gpu_paged_attention derives, and
+for scales near 2^-127 the step of their products with weights, 2^-149 each, times
+a code of at most 448."""
 import math
 
 import pytest
@@ -11,6 +13,7 @@ import approximate_top_selection_b200 as atk
 pytestmark = pytest.mark.gpu
 
 DEV = "cuda:0"
+E4M3 = torch.float8_e4m3fn
 U = 2.0 ** -24
 
 
@@ -66,6 +69,8 @@ def reference(s, scale=None):
         o, mass = p @ (v * vs[..., None]), p @ (v * vs[..., None]).abs()
         weights = (2.0 ** -11 if e4m3 else 2.0 ** -16)
         tol = 2.0 ** -8 * o.abs() + 2.0 ** -134 + (2 * size * (2 * d + 2) * U + 2.0 ** -20 + weights + 2 * U * (n + 64)) * mass
+        if e4m3:
+            tol = tol + n * 448 * 2.0 ** -149
         outs.append(o.reshape(heads, d))
         tols.append(tol.reshape(heads, d))
         lses.append(torch.logsumexp(t, 2).reshape(heads))
@@ -124,3 +129,31 @@ def test_infinite_values_of_small_weights(heads, d):
         s["v"][key // 16, 0, key % 16, col] = math.inf
     out, _ = call(s, scale=math.log(2.0))  # scores are powers of two's exponents
     assert bool((out[..., :4] == math.inf).all()) and bool(torch.isfinite(out[..., 4:]).all())
+
+
+def quantised(s, k_exp=(-9, -5), v_exp=(-9, -5), seed=5):
+    g = torch.Generator(device=DEV).manual_seed(seed)
+    for n, (lo, hi) in (("k", k_exp), ("v", v_exp)):
+        s[n + "_scale"] = torch.exp2(torch.randint(lo, hi, s[n].shape[:3], generator=g, device=DEV).double()).float()
+        s[n] = (s[n].float() * 100).clamp(-448, 448).to(E4M3)
+    return s
+
+
+@pytest.mark.parametrize("batch,heads,kv_heads,d,n", [(2, 4, 4, 64, 30), (1, 8, 2, 128, 3000), (60, 8, 8, 128, 40),
+                                                      (2, 16, 1, 256, 600)])
+@pytest.mark.parametrize("lowest,above", [(-127, 1), (-127, 30), (-120, 4), (110, 10)])
+def test_smallest_and_largest_value_scales(batch, heads, kv_heads, d, n, lowest, above):
+    """Scales as cache_write leaves them for rows of the smallest and the largest bf16 values."""
+    check(quantised(contiguous(batch, heads, kv_heads, d, [n] * batch, n), v_exp=(lowest, lowest + above)))
+
+
+def test_written_rows_of_tiny_values_come_back_through_attention():
+    s = contiguous(1, 2, 2, 128, [64], 8)
+    v = (s["v"].double() * 2.0 ** -119).bfloat16()
+    kc, vc = (torch.zeros(4, 2, 16, 128, device=DEV).to(E4M3) for _ in range(2))
+    ks, vs = (torch.ones(4, 2, 16, device=DEV) for _ in range(2))
+    new = [x.transpose(1, 2).reshape(64, 2, 128).contiguous() for x in (s["k"], v)]
+    atk.cache_write(*new, kc, vc, torch.arange(64, device=DEV), k_scale=ks, v_scale=vs)
+    t = {**s, "k": kc, "v": vc, "k_scale": ks, "v_scale": vs}
+    check(t)
+    assert float(call(t)[0].abs().max()) > 2.0 ** -122
