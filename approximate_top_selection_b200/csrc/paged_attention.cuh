@@ -302,6 +302,7 @@ struct AttendWarp {
 
   // The smallest f, whose inverse is finite: the smallest scale, 2^-127, is half of it.
   static constexpr float kLeast = 1.17549435e-38f;  // 2^-126
+  static constexpr float kMost = 3.40282347e38f;    // of a finite w
 
   static __device__ __forceinline__ int key_of(int r) {
     return kE4m3 ? ((r & 6) << 1) + (r & 1) + ((r >> 2) & 2) : r;
@@ -513,9 +514,11 @@ struct AttendWarp {
         }
       }
     if constexpr (kE4m3) {
-      // w_j = p_j * vscale_j, held in f16 relative to f: f follows the largest
-      // w of the head, so the weights that carry the sum keep 11 bits whatever
-      // the scales are.
+      // w_j = p_j * vscale_j, held in f16 relative to f, which is at most 2^-10 of
+      // the head's largest w: a weight keeps 11 bits down to 2^-24 of that, and
+      // below is off by 2^-35 of it at most.  (With f at the largest w itself, the
+      // tail behind a key of 2^24 times its weight was off by 20 % where that key's
+      // value is 0.)  f16 holds up to 65504, so f moves when a w passes 2^15 f.
       float wt[NT][2];
 #pragma unroll
       for (int n = 0; n < NT; ++n) wt[n][0] = wt[n][1] = 0.0f;
@@ -536,13 +539,13 @@ struct AttendWarp {
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
-        for (int h = 0; h < 2; ++h) grow |= wt[n][h] > f[n][h] * 256.0f;
+        for (int h = 0; h < 2; ++h) grow |= wt[n][h] > f[n][h] * 32768.0f;
       if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            const float fn = fmaxf(f[n][h], fminf(column_max(wt[n][h]), 8e37f));  // 1 / f is to be no subnormal
+            const float fn = fmaxf(f[n][h], fminf(column_max(wt[n][h]), kMost) * 0x1p-10f);
             const float x = f[n][h] / fn;
             f[n][h] = fn;
             inv[n][h] = 1.0f / fn;

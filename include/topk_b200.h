@@ -308,9 +308,11 @@ int cache_read(const topk_cache *cache, const int32_t *block_table_dev, int64_t 
  * p = softmax over j of scale * q[b][h] . K_j, and lse[b][h] = log sum_j
  * exp(scale * q[b][h] . K_j), over the tokens j < seq_lens[b], or over the
  * listed positions.  Query head h reads key-value head h / (heads / kv_heads).
- * Products, sums and softmax are float32 (a weight enters its product with V
- * with 16 significant bits beside BF16 values, 11 beside E4M3 ones); out is
- * rounded once to bf16.  Equal calls give equal bits.
+ * Products, sums and softmax are float32.  A weight enters its product with V
+ * with 16 significant bits beside BF16 values.  Beside E4M3 ones it is p_j times
+ * the row's scale, with 11 significant bits down to 2^-24 of the largest such
+ * product of the head, and within 2^-35 of that below.  out is rounded once to
+ * bf16.  Equal calls give equal bits.
  *   q_dev         bf16, sequence b at b * q_stride elements, [heads x d]
  *                 contiguous there; 16-byte aligned, q_stride a multiple of 8.
  *   heads         a multiple of kv_heads.

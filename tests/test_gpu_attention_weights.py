@@ -1,8 +1,10 @@
 """Attention where the weights or the values span more than a float's bits.
 
-The bound on an output is the one that test_gpu_paged_attention derives, and
-for scales near 2^-127 the step of their products with weights, 2^-149 each, times
-a code of at most 448."""
+The bound on an output is the one that test_gpu_paged_attention derives.  Beside
+e4m3 codes a weight w_j = p_j * scale_j has 11 significant bits (2^-11 w_j), or lies
+below 2^-24 of the head's largest, W, and is off by half a step at most, 2^-35 W;
+products of scales near 2^-127 and weights are multiples of 2^-149.  Both times the
+column's largest code."""
 import math
 
 import pytest
@@ -70,7 +72,8 @@ def reference(s, scale=None):
         weights = (2.0 ** -11 if e4m3 else 2.0 ** -16)
         tol = 2.0 ** -8 * o.abs() + 2.0 ** -134 + (2 * size * (2 * d + 2) * U + 2.0 ** -20 + weights + 2 * U * (n + 64)) * mass
         if e4m3:
-            tol = tol + n * 448 * 2.0 ** -149
+            largest = (p * vs[:, None]).abs().amax(2, keepdim=True)
+            tol = tol + n * v.abs().amax(1, keepdim=True) * (2.0 ** -35 * largest + 2.0 ** -149)
         outs.append(o.reshape(heads, d))
         tols.append(tol.reshape(heads, d))
         lses.append(torch.logsumexp(t, 2).reshape(heads))
@@ -157,3 +160,47 @@ def test_written_rows_of_tiny_values_come_back_through_attention():
     t = {**s, "k": kc, "v": vc, "k_scale": ks, "v_scale": vs}
     check(t)
     assert float(call(t)[0].abs().max()) > 2.0 ** -122
+
+
+@pytest.mark.parametrize("batch,heads,kv_heads,d,n", [
+    (450, 4, 1, 128, 1000),  # whole sequences by warps
+    (400, 16, 1, 64, 500),
+    (24, 8, 2, 128, 9000),   # sequences shared by CTAs
+    (40, 1, 1, 256, 3000),
+    (20, 16, 1, 256, 3000),
+    (1, 4, 1, 128, 131072),
+])
+@pytest.mark.parametrize("ahead", [5.0, 8.3, 11.0, 16.2, 17.2, 19.0])
+def test_a_key_that_outweighs_a_long_tail(batch, heads, kv_heads, d, n, ahead):
+    """All scores are equal but one, `ahead` larger, whose values are zero in
+    half of the columns: there the tail is all there is."""
+    s = quantised(contiguous(batch, heads, kv_heads, d, [n] * batch, n))
+    s["q"][:] = 0
+    s["q"][..., 0] = 1.0
+    s["k"].view(torch.uint8)[:] = 0
+    s["v_scale"][:] = 2.0 ** -7
+    s["v"].view(torch.uint8)[:] = 0x38  # 1.0
+    width = s["table"].shape[1]
+    for b in range(batch):
+        key = (77 * b + n // 2) % n
+        page, off = b * width + key // 16, key % 16
+        s["k"].view(torch.uint8)[page, :, off, 0] = 0x38
+        s["k_scale"][page, :, off] = 1.0
+        s["v"].view(torch.uint8)[page, :, off, ::2] = 0
+    check(s, scale=ahead)
+
+
+def test_value_scales_far_apart():
+    for heads, kv_heads, d, n in ((8, 2, 128, 5000), (3, 3, 64, 700), (16, 1, 128, 2000), (4, 4, 256, 3000)):
+        check(quantised(contiguous(3, heads, kv_heads, d, [n, n // 3, 9], n), v_exp=(-30, -4)))
+        check(quantised(contiguous(3, heads, kv_heads, d, [n, n // 3, 9], n), v_exp=(-100, 100)))
+
+
+def test_scales_and_codes_of_the_values_against_each_other():
+    """Half of the keys have scales 2^-20 of the others' and values where the others have none."""
+    s = quantised(contiguous(2, 8, 2, 128, [900, 4000], 4))
+    s["v"].view(torch.uint8)[:] = 0x40  # 2.0
+    s["v_scale"][:] = 2.0 ** -6
+    s["v_scale"][:, :, ::2] = 2.0 ** -26
+    s["v"].view(torch.uint8)[:, :, 1::2, ::3] = 0
+    check(s)
