@@ -230,8 +230,8 @@ def paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
     kv_heads, page_size] float32; heads is a multiple of kv_heads.  block_table:
     [batch, width] int32 page numbers; seq_lens: [batch] int32.  positions:
     None for all tokens, or [batch, lists, c] int32 token positions (as
-    score_topk and score_rerank return them; negative = empty), list l serving
-    heads l * heads / lists and on.  scale: 1 / sqrt(d) unless given.
+    score_topk and score_rerank return them; negative = empty, at or behind the
+    sequence's end = left out), list l serving heads l * heads / lists and on.  scale: 1 / sqrt(d) unless given.
     Returns out [batch, heads, d] bfloat16, or (out, lse [batch, heads]
     float32).  A head with nothing to attend to gives zeros and -inf.
     """
@@ -332,7 +332,9 @@ def cache_read(cache: torch.Tensor, block_table: torch.Tensor, seq_lens: torch.T
     """The first n tokens of every sequence as contiguous rows [batch, kv_heads, n, d] bfloat16.
 
     Rows behind a sequence's end are zeros.  `out.view(-1, n, d)` is the key
-    matrix per row that score_topk and score_rerank take.
+    matrix per row that score_topk and score_rerank take, for sequences of n
+    tokens or more: a row of zeros scores 0, above every key of negative score.
+    Sequences of unlike lengths take calls of their own (the README shows one).
     """
     if stream is None and out is None:
         made = (_calls or _usual()).cache_read(cache, block_table, seq_lens, n, scale)

@@ -289,7 +289,10 @@ int cache_write(const uint16_t *k_dev, int64_t k_token_stride, int64_t k_head_st
 
 /* Reads the first n tokens of every sequence back as contiguous bf16 rows:
  * out[b][h][t] for t < min(n, seq_lens[b]), zeros behind.  With batch *
- * kv_heads rows of [n x d] keys this is what score_topk and score_rerank take.
+ * kv_heads rows of [n x d] keys this is what score_topk and score_rerank take,
+ * for sequences of n tokens or more: they know no lengths, and a row of zeros
+ * behind a sequence's end scores 0, above every key of negative score.  Read and
+ * select from sequences of unlike lengths in calls of their own.
  * An E4M3 value is code * scale rounded once to bf16 (exact for the scales of
  * cache_write).
  *   block_table_dev  [batch] rows of table_width int32 page numbers, row b at
