@@ -418,7 +418,9 @@ def beam_reorder(states, parents: torch.Tensor, *, out=None, stream=None):
     states: a contiguous tensor [batch, beams, ...] of any dtype, or a list or
     tuple of up to 256 of them; parents: [batch, k] int32.  Returns the same
     with [batch, k, ...]: row (b, j) is row (b, parents[b, j]), zeros where
-    that is -1.  `out` (of the same form) must not overlap the states.
+    that is -1.  `out` (of the same form) must not overlap the states.  Of a page
+    table, rows of one parent name the same pages: copy a page that is not full
+    before the next token is written into it (the README shows it).
     """
     one = isinstance(states, torch.Tensor)
     if stream is None and out is None:

@@ -396,7 +396,10 @@ size_t topk_beam_workspace_bytes(int64_t batch, int beams, int64_t n, int k);
 /* Brings per-beam states into the order topk_beam chose: for every tensor s
  * and new beam (b, j), row dst[s][b][j] = row src[s][b][parents[b][j]].  A
  * parent of -1 (a slot topk_beam left empty) gives a row of zeros; any other
- * parent outside [0, beams) does too and sets TOPK_DEV_BAD_INDEX.
+ * parent outside [0, beams) does too and sets TOPK_DEV_BAD_INDEX.  Page tables
+ * are such states: beams of one parent then share pages, and of a page that is
+ * not full each needs a copy before cache_write puts its next token there (a row
+ * of zeros names page 0: the beam it stands for is to write nowhere).
  *   src, dst     HOST arrays of `count` device pointers, 1 <= count <= 256
  *                (else TOPK_EUNSUPPORTED); any alignment.
  *   row_bytes    HOST array [count]: bytes of one beam's row, contiguous; src[s]
