@@ -437,7 +437,9 @@ def beam_reorder(states, parents: torch.Tensor, *, out=None, stream=None):
     batch, k = parents.shape
     beams = 0
     sizes = []
-    for t in src:
+    for i, t in enumerate(src):
+        if isinstance(t, torch.Tensor) and (t.is_conj() or t.is_neg()):  # bytes that stand for something else
+            t = src[i] = t.resolve_conj().resolve_neg()
         if not isinstance(t, torch.Tensor) or t.get_device() != dev or not t.is_contiguous():
             _cuda(t, "states", t.dtype if isinstance(t, torch.Tensor) else None)
             _same_device(parents, states=t)
@@ -457,6 +459,8 @@ def beam_reorder(states, parents: torch.Tensor, *, out=None, stream=None):
         for t, o in zip(src, out):
             _cuda(o, "out", t.dtype)
             _same_device(parents, out=o)
+            if o.is_conj() or o.is_neg():
+                raise ValueError("out must not be a conjugate or negative view")
             if tuple(o.shape) != (batch, k) + tuple(t.shape[2:]):
                 raise ValueError("out must be [batch, k, ...]")
 

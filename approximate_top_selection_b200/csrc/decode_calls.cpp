@@ -301,7 +301,7 @@ PyObject* call_reorder(PyObject*, PyObject* const* a, Py_ssize_t n) {
     for (Py_ssize_t i = 0; i < m; ++i) {
       const at::Tensor& t = tensor(items[i]);
       usual(t.is_cuda() && t.get_device() == dev && t.layout() == at::kStrided && t.dim() >= 2 && t.is_contiguous() &&
-            t.numel() > 0 && t.size(0) == batch && (i == 0 || t.size(1) == beams) && t.size(1) <= INT32_MAX);
+            !t.is_conj() && !t.is_neg() && t.numel() > 0 && t.size(0) == batch && (i == 0 || t.size(1) == beams) && t.size(1) <= INT32_MAX);
       beams = t.size(1);
       shape.assign(t.sizes().begin(), t.sizes().end());
       shape[1] = k;
