@@ -210,6 +210,21 @@ def _workspace_bytes(query, *sizes) -> int:
     return n
 
 
+def _given_workspace(t, first: torch.Tensor) -> None:
+    """A workspace handed in: its bytes have to be there, so no view of fewer."""
+    if t is None:
+        return
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError("workspace must be a CUDA tensor")
+    if not t.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    _same_device(first, workspace=t)
+
+
+def _bytes(t: torch.Tensor) -> int:
+    return t.numel() * t.element_size()
+
+
 def _pointer(t):
     return t.data_ptr() if t is not None else None
 
@@ -263,8 +278,7 @@ def paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
         if lists < 1 or c < 1 or lists % kv_heads or heads % lists:
             raise ValueError("positions needs c >= 1 and lists a multiple of kv_heads that divides heads")
     _int32(heads=heads, lists=lists, c=c)
-    if workspace is not None:
-        _same_device(q, workspace=workspace)
+    _given_workspace(workspace, q)
 
     def body(out, out_lse, ws, sh):
         out = _out(out, shape, _BF16, "out", dev)
@@ -275,7 +289,7 @@ def paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
         _check(load_library().paged_attention(
             q.data_ptr(), strides[0], batch, heads, ctypes.byref(kc), ctypes.byref(vc), block_table.data_ptr(),
             table_stride, width, seq_lens.data_ptr(), _pointer(positions), lists, c,
-            d ** -0.5 if scale is None else scale, out.data_ptr(), _pointer(out_lse), ws.data_ptr(), ws.numel(), sh),
+            d ** -0.5 if scale is None else scale, out.data_ptr(), _pointer(out_lse), ws.data_ptr(), _bytes(ws), sh),
             "paged_attention")
         return (out, out_lse) if return_lse else out
 
@@ -390,8 +404,7 @@ def topk_beam(logits: torch.Tensor, beam_scores: torch.Tensor, k: int, *, out_sc
         if logits.dim() != 3 or tuple(beam_scores.shape) != tuple(logits.shape[:2]):
             raise ValueError("logits must be [batch, beams, n] and beam_scores [batch, beams]")
         _same_device(logits, beam_scores=beam_scores)
-    if workspace is not None:
-        _same_device(logits, workspace=workspace)
+    _given_workspace(workspace, logits)
     batch, beams, n = logits.shape
     _int32(beams=beams, k=k)
 
@@ -406,7 +419,7 @@ def topk_beam(logits: torch.Tensor, beam_scores: torch.Tensor, k: int, *, out_sc
         lib = load_library()
         fn = lib.topk_beam_bf16 if bf16 else lib.topk_beam
         _check(fn(logits.data_ptr(), beam_scores.data_ptr(), batch, beams, n, k, out_scores.data_ptr(),
-                  out_parent.data_ptr(), out_token.data_ptr(), ws.data_ptr(), ws.numel(), sh), "topk_beam")
+                  out_parent.data_ptr(), out_token.data_ptr(), ws.data_ptr(), _bytes(ws), sh), "topk_beam")
         return out_scores, out_parent, out_token
 
     return _on(dev, stream, body, out_scores, out_parent, out_token, workspace)
