@@ -489,9 +489,11 @@ __global__ void __launch_bounds__(kBeamThreads) beam_finish_kernel(BeamArgs p) {
       top = max(top, __reduce_max_sync(0xffffffffu, raw.z));
       by_max |= __any_sync(0xffffffffu, raw.z && rj == kBeamByMax);
       const int now = max(j0 ? r : kBeamByMax, __reduce_max_sync(0xffffffffu, raw.z ? rj : kBeamByMax));
-      // differences beyond 1100 leave nothing of a sum below 2^32
-      if (j0) sum = scalbn(sum, max(r - now, -1100));
-      if (raw.z) sum += scalbn(x, max(rj - now, -1100));
+      // Differences beyond 1100 leave nothing of a sum below 2^32.  No piece so
+      // far, or one by its maximum, has no r to subtract from.
+      auto down = [now](int from) { return from == kBeamByMax ? -1100 : max(from - now, -1100); };
+      if (j0) sum = scalbn(sum, down(r));
+      if (raw.z) sum += scalbn(x, down(rj));
       r = now;
     }
     const bool bad = top >= 0xff800000u;  // +inf or NaN

@@ -118,3 +118,22 @@ def test_beams_four_bounds_apart_keep_their_order(dtype):
     assert int(clear.sum()) > batch // 2
     _, parent, _ = atk.topk_beam(x, s, 2)
     assert torch.equal(parent[clear, 0].long(), exact.argmax(1)[clear])
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("huge", [False, True])
+def test_forbidden_stretches_before_the_first_token(dtype, huge):
+    """Many pieces of a row without a token, before those that have some."""
+    n, first = 262143, 170001
+    g = torch.Generator(device=DEV).manual_seed(4)
+    x = torch.full((1, 1, n), -math.inf, device=DEV)
+    x[..., first:] = torch.randn(n - first, generator=g, device=DEV)
+    if huge:
+        x[..., first + 50000:] -= 3e6  # pieces summed relative to their own maximum
+    x = x.to(dtype)
+    lse = torch.logsumexp(x.double().flatten(), 0)
+    s = (lse - x.double().max()).float().view(1, 1)
+    val, _, token = atk.topk_beam(x, s, 3)
+    best = (x.double().flatten() + s.double().flatten() - lse).sort(descending=True, stable=True)
+    assert bool(((val.double().flatten() - best.values[:3]).abs() <= LSE + 2.0 ** -24 * best.values[:3].abs()).all())
+    assert torch.equal(token.flatten().long(), best.indices[:3])
