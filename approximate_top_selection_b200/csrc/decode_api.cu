@@ -143,10 +143,9 @@ int launch_attend(AttendArgs& a, const DeviceInfo& dev, cudaStream_t st) {
 }
 
 template <int D, bool kE4m3>
-int launch_write(const WriteArgs& a, const DeviceInfo& dev, cudaStream_t st) {
+int launch_write(const WriteArgs& a, cudaStream_t st) {
   int rc = prepare_kernel(cache_write_kernel<D, kE4m3>);
   if (rc) return rc;
-  (void)dev;
   const int64_t blocks = (a.tokens + kWriteTokens - 1) / kWriteTokens;
   if (blocks > kMaxGridX) return TOPK_EUNSUPPORTED;
   const int lines = (2 * a.cache[0].kv_heads + write_lines<D>() - 1) / write_lines<D>();
@@ -155,10 +154,9 @@ int launch_write(const WriteArgs& a, const DeviceInfo& dev, cudaStream_t st) {
 }
 
 template <int D, bool kE4m3>
-int launch_read(const ReadArgs& a, const DeviceInfo& dev, cudaStream_t st) {
+int launch_read(const ReadArgs& a, cudaStream_t st) {
   int rc = prepare_kernel(cache_read_kernel<D, kE4m3>);
   if (rc) return rc;
-  (void)dev;
   const int64_t blocks = (a.n + read_rows<D>() - 1) / read_rows<D>();
   return launch_pdl(cache_read_kernel<D, kE4m3>,
                     dim3(static_cast<unsigned>(blocks), static_cast<unsigned>(std::min(a.cache.kv_heads, 65535)),
@@ -335,8 +333,6 @@ int cache_write(const uint16_t* k, int64_t k_token_stride, int64_t k_head_stride
   const int64_t strides[4] = {k_token_stride, k_head_stride, v_token_stride, v_head_stride};
   for (int64_t s : strides)
     if (s < 0 || s > kMaxElems || s % 8) return TOPK_EINVAL;
-  DeviceInfo dev;
-  if ((rc = current_device_info(&dev))) return rc;
   a.src[0] = k;
   a.src[1] = v;
   a.token_stride[0] = k_token_stride;
@@ -345,7 +341,7 @@ int cache_write(const uint16_t* k, int64_t k_token_stride, int64_t k_head_stride
   a.head_stride[1] = v_head_stride;
   a.slots = slots;
   a.tokens = tokens;
-  return TK_BY_CACHE(launch_write, k_cache->d, a.cache[0].scale != nullptr, a, dev, static_cast<cudaStream_t>(stream));
+  return TK_BY_CACHE(launch_write, k_cache->d, a.cache[0].scale != nullptr, a, static_cast<cudaStream_t>(stream));
 }
 
 int cache_read(const topk_cache* cache, const int32_t* block_table, int64_t table_stride, int table_width,
@@ -357,11 +353,9 @@ int cache_read(const topk_cache* cache, const int32_t* block_table, int64_t tabl
   if ((rc = table_view(block_table, table_stride, table_width, seq_lens, batch, cache->page_size, &a.tab))) return rc;
   if (batch > kMaxElems / cache->kv_heads / n / cache->d) return TOPK_EUNSUPPORTED;
   if (!aligned16(out)) return TOPK_EINVAL;
-  DeviceInfo dev;
-  if ((rc = current_device_info(&dev))) return rc;
   a.n = n;
   a.out = out;
-  return TK_BY_CACHE(launch_read, cache->d, a.cache.scale != nullptr, a, dev, static_cast<cudaStream_t>(stream));
+  return TK_BY_CACHE(launch_read, cache->d, a.cache.scale != nullptr, a, static_cast<cudaStream_t>(stream));
 }
 
 size_t topk_beam_workspace_bytes(int64_t batch, int beams, int64_t n, int k) {

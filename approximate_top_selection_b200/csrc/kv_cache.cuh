@@ -54,14 +54,8 @@ __device__ __forceinline__ int seq_length(const TableView& t, int b) {
   return n;
 }
 
-// Two e4m3 codes as two f16 values (exact: 4 significant bits, exponents -9 .. 8).
-__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t two) {
-  uint32_t r;
-  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(static_cast<uint16_t>(two)));
-  return r;
-}
-
-// Four codes: the lower two and the upper two of a word.
+// Four e4m3 codes as f16 values (exact: 4 significant bits, exponents -9 .. 8): the
+// lower two and the upper two of a word.
 __device__ __forceinline__ void e4m3x4_to_f16x2(uint32_t four, uint32_t& low, uint32_t& high) {
   asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %2;\n\t"
       "cvt.rn.f16x2.e4m3x2 %0, lo;\n\tcvt.rn.f16x2.e4m3x2 %1, hi;\n\t}"
