@@ -246,7 +246,10 @@ def paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
     [batch, width] int32 page numbers; seq_lens: [batch] int32.  positions:
     None for all tokens, or [batch, lists, c] int32 token positions (as
     score_topk and score_rerank return them; negative = empty, at or behind the
-    sequence's end = left out), list l serving heads l * heads / lists and on.  scale: 1 / sqrt(d) unless given.
+    sequence's end = left out), list l serving heads l * heads / lists and on.
+    scale: 1 / sqrt(d) unless given.
+    The table's width stands for the longest length: a slice of the columns that
+    the batch needs serves many short sequences fastest.
     Returns out [batch, heads, d] bfloat16, or (out, lse [batch, heads]
     float32).  A head with nothing to attend to gives zeros and -inf.
     """
@@ -348,7 +351,7 @@ def cache_read(cache: torch.Tensor, block_table: torch.Tensor, seq_lens: torch.T
     Rows behind a sequence's end are zeros.  `out.view(-1, n, d)` is the key
     matrix per row that score_topk and score_rerank take, for sequences of n
     tokens or more: a row of zeros scores 0, above every key of negative score.
-    Sequences of unlike lengths take calls of their own (the README shows one).
+    Sequences of unlike lengths take calls of their own, each with its length as n.
     """
     if stream is None and out is None:
         made = (_calls or _usual()).cache_read(cache, block_table, seq_lens, n, scale)
@@ -432,8 +435,8 @@ def beam_reorder(states, parents: torch.Tensor, *, out=None, stream=None):
     tuple of up to 256 of them; parents: [batch, k] int32.  Returns the same
     with [batch, k, ...]: row (b, j) is row (b, parents[b, j]), zeros where
     that is -1.  `out` (of the same form) must not overlap the states.  Of a page
-    table, rows of one parent name the same pages: copy a page that is not full
-    before the next token is written into it (the README shows it).
+    table, rows of one parent name the same pages: of a page that is not full each
+    needs a copy of its own before the next token is written into it.
     """
     one = isinstance(states, torch.Tensor)
     if stream is None and out is None:

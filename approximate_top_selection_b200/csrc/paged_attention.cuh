@@ -9,9 +9,10 @@
 // it, eight or sixteen at a time: they are the columns of the matrix products
 // S^T = K Q^T (16 keys x 8 heads) and O^T += V^T P^T (16 columns of V x 8
 // heads), so that a head that shares its keys with none wastes seven eighths of
-// the small operand, not of the large one.  16 flops per element of K and V and
-// group of eight heads: 51 TFLOP/s of bf16 at full bandwidth.  The kernel is
-// bound by reading K and V from HBM.
+// the small operand, not of the large one.  16 flops per element of K and of e4m3
+// V, 32 of bf16 V (a weight has two parts there), and group of eight heads: 78
+// TFLOP/s of bf16 at full bandwidth.  The kernel is bound by reading K and V
+// from HBM.
 //
 // Work: a unit is (sequence, list of query heads); its tokens are cut into
 // granules of 4 * KT tokens, one tile of KT keys per warp.  All granules of
@@ -32,12 +33,12 @@
 // twice the time of the products on lists of 512 positions).
 //
 // Measured on one B200, bytes of K, V and scales against its copy bandwidth of
-// 6461 GB/s: 16 ragged sequences up to 32768, 32 heads on 8, d 128, bf16: 196
-// us, 98 %; 16 x 8192, 32 on 32: 197 us, 98 %; pages of one token: 197 us, 98 %;
-// e4m3, 4 ragged sequences up to 131072: 118 us, 87 % (issue: the codes' widening);
-// 512 of 8192 positions for 512 heads: 34 us, 61 % (starts, ends and joins of
-// 13 tiles a warp); 128 heads on 8 (NT = 2): bf16 209 us, 92 %, e4m3 159 us, 63 %
-// (issue).  One sequence of 1001: 11 us, of which the work takes 1: about 4 us
+// 6461 GB/s: 16 ragged sequences up to 32768, 32 heads on 8, d 128, bf16: 196 to
+// 203 us on several GPUs, 98 to 95 %; 16 x 8192, 32 on 32: 197 us, 98 %; pages of
+// one token: 197 us, 98 %; e4m3, 4 ragged sequences up to 131072: 118 us, 87 %
+// (issue: the codes' widening); 512 of 8192 positions for 512 heads: 34 us, 61 %,
+// e4m3 30 us, 36 % (starts, ends and joins of 13 tiles a warp); 128 heads on 8
+// (NT = 2): bf16 211 us, 92 %, e4m3 162 us, 62 % (issue).  One sequence of 1001: 11 us, of which the work takes 1: about 4 us
 // pass before the first tile (lengths, table, rows are three dependent trips to
 // memory), about 4 in joining 16 parts.
 // Rejected: heads as the 16 rows of the products (237 us where this takes 196:
